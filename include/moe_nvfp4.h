@@ -56,8 +56,10 @@ typedef enum {
     MOE_ERR_SCALE = 9,             /* device: a weight block scale the tensor-core     */
                                    /*   kernels cannot read (sign bit set, or NaN;    */
                                    /*   found by moe_workspace_init's scan)           */
-    MOE_ERR_WORKSPACE_BUSY = 10    /* host: another thread is launching on the        */
+    MOE_ERR_WORKSPACE_BUSY = 10,   /* host: another thread is launching on the        */
                                    /*   workspace from another stream                 */
+    MOE_ERR_BAD_INDEX = 11         /* device: a page id, position or sequence offset  */
+                                   /*   out of range (moe_layer.h; see moe_kv_check)  */
 } moe_status_t;
 
 /* Opaque plan: host memory owned by the library (moe_plan_destroy frees it). */

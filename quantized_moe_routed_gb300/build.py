@@ -1,6 +1,6 @@
 """Build the sm_103a C-ABI library libmoe_nvfp4.so in-tree (nvcc, no cmake).
 
-The four translation units compile in parallel, then link into
+The translation units compile in parallel, then link into
 quantized_moe_routed_gb300/_build/libmoe_nvfp4.so (static cudart).  The
 compiler's output for each unit (the kernels' ptxas register and spill report)
 is kept beside the objects as <unit>.log.
@@ -17,8 +17,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_nvfp4.so")
-SOURCES = ("moe_kernels.cu", "moe_tc.cu", "moe_small.cu", "moe_gemv.cu", "moe_route.cu", "moe_abi.cu")
-HEADERS = ("moe_internal.h", "moe_device.cuh", "moe_tcgen05.cuh")
+SOURCES = ("moe_kernels.cu", "moe_tc.cu", "moe_small.cu", "moe_gemv.cu", "moe_route.cu", "moe_abi.cu",
+           "moe_norm.cu", "moe_linear.cu", "moe_kv_append.cu", "moe_kv_attend.cu", "moe_layer.cu")
+HEADERS = ("moe_internal.h", "moe_device.cuh", "moe_tcgen05.cuh", "moe_host.h", "moe_layer_internal.h",
+           "moe_layer_device.cuh")
+ABI = ("moe_nvfp4.h", "moe_layer.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,7 +36,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "moe_nvfp4.h")]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", f) for f in ABI]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -48,7 +51,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         cmd = [cc] + common + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if src in ("moe_kernels.cu", "moe_tc.cu", "moe_small.cu", "moe_gemv.cu", "moe_route.cu"):
+        if src not in ("moe_abi.cu", "moe_layer.cu"):
             cmd += ["-Xptxas", "-v"]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         objs.append(obj)

@@ -2,10 +2,10 @@
 // argument validation, tile choice, workspace layout, launches, counters.
 // Every step of the computation runs in the kernels (moe_kernels.cu,
 // moe_tc.cu, moe_route.cu); this file only checks, plans and enqueues.
+#include "moe_host.h"
 #include "moe_internal.h"
 #include "moe_nvfp4.h"
 
-#include <cudaTypedefs.h>
 #include <algorithm>
 
 #include <cstdarg>
@@ -20,6 +20,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace moe {
+
 moe_status_t fail(moe_status_t s, const char *fmt, ...)
 {
     char buf[512];
@@ -31,7 +35,18 @@ moe_status_t fail(moe_status_t s, const char *fmt, ...)
     return s;
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace moe
+
+namespace {
+
+using moe::aligned;
+using moe::encoder;
+using moe::encode_rows;
+using moe::fail;
+using moe::ws_claim;
+using moe::ws_release;
+using moe::WsTicket;
+
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int align16i(int v) { return (v + 15) & ~15; }
 
@@ -43,6 +58,10 @@ bool env_flag(const char *name)
 
 std::once_flag g_active_once;
 std::once_flag g_gv_once;
+
+}  // namespace
+
+namespace moe {
 
 // ------------------------------------------------------------------ workspace ownership
 // Which stream each workspace was last launched on, with an event recorded
@@ -60,13 +79,10 @@ struct WsUse {
     bool recorded = false;
     int pending = 0;  // claims on st not yet released
 };
+namespace {
 std::mutex g_ws_mu;
 WsUse g_ws[64];
-
-struct WsTicket {
-    WsUse *u = nullptr;  // null: not tracked (graph capture)
-    cudaStream_t st = nullptr;
-};
+}  // namespace
 
 moe_status_t ws_claim(const void *ws, cudaStream_t st, WsTicket &t)
 {
@@ -144,7 +160,42 @@ void ws_release(WsTicket &t, bool launched)
     t.u = nullptr;
 }
 
-}  // namespace
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+CUresult encode_rows(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, int box_c, int box_r, bool sw128)
+{
+    const cuuint32_t es[2] = {1, 1};
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_c), static_cast<cuuint32_t>(box_r)};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     sw128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+long long wait_limit_ns()
+{
+    if (const char *t = std::getenv("MOE_WAIT_TIMEOUT_MS")) {
+        const long long ms = std::atoll(t);
+        if (ms > 0) return ms * 1000000LL;
+    }
+    return 1000000000LL;
+}
+
+}  // namespace moe
 
 // One tiling of the step kernel: gate/up tiles of RA rows and K parts of KA
 // elements, down parts of KB elements, the stage sub-buffer offsets and the
@@ -238,21 +289,6 @@ bool choose_part(int K, int cap, int cap_odd, PartPlan *pp)
 }
 
 int up1024(int v) { return (v + 1023) / 1024 * 1024; }
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
 
 // E2M1 rows [rows_total, K/2 bytes].  Mode 0: a 3-D view {64 B, rows, K/128
 // spans} whose box {64, BR, KP/128} lands span-major ([span][row][64 B]);
@@ -420,18 +456,6 @@ moe_status_t build_tc_maps(const moe_plan_desc &d, const WeightSet &w, CUtensorM
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "tensor-map encoding for the tensor-core kernel failed (CUresult %d)",
                     static_cast<int>(cr));
     return MOE_OK;
-}
-
-// Row-major uint8 [rows, cols] with a {box_c, box_r} box.
-CUresult encode_rows(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, int box_c, int box_r, bool sw128)
-{
-    const cuuint32_t es[2] = {1, 1};
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_c), static_cast<cuuint32_t>(box_r)};
-    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     sw128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // MMA N (digit rows per group) for a launch of T tokens: a group holds at
@@ -1127,6 +1151,7 @@ const char *moe_status_string(moe_status_t s)
         case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT";
         case MOE_ERR_BAD_EXPERT_ID: return "MOE_ERR_BAD_EXPERT_ID";
         case MOE_ERR_RANGE: return "MOE_ERR_RANGE";
+        case MOE_ERR_BAD_INDEX: return "MOE_ERR_BAD_INDEX";
     }
     return "MOE_ERR_UNKNOWN";
 }
@@ -1191,10 +1216,7 @@ moe_status_t moe_plan_create(const moe_plan_desc *desc, moe_plan_t *out)
     pl->smem_optin = optin;
     pl->strict = d.strict != 0 || env_flag("MOE_STRICT");
     pl->pdl = d.pdl != 0;
-    if (const char *t = std::getenv("MOE_WAIT_TIMEOUT_MS")) {
-        const long long ms = std::atoll(t);
-        if (ms > 0) pl->timeout_ns = ms * 1000000LL;
-    }
+    pl->timeout_ns = moe::wait_limit_ns();
     if (!encoder()) {
         delete pl;
         return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
