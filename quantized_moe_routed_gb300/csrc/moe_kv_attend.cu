@@ -423,26 +423,36 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 if (lane == 0) mbar_arrive(&ct->empty[st]);
                 continue;
             }
+            // the products go step by step over eight independent accumulators, so
+            // that an MMA's latency is covered by the ones beside it
             float sc[8][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int tok = 16 * (g >> 1) + 2 * j + (g & 1);
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
-                uint4 w[KS / 2];
 #pragma unroll
-                for (int i = 0; i < KS / 2; ++i) {
+            for (int i = 0; i < KS / 2; ++i) {
+                uint4 w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int tok = 16 * (g >> 1) + 2 * j + (g & 1);
                     const int gr = D == 128 ? ((2 * t4 + i) ^ (tok & 7)) : t4;
-                    w[i] = *reinterpret_cast<const uint4 *>(kp + tok * D + gr * 16);
+                    w[j] = *reinterpret_cast<const uint4 *>(kp + tok * D + gr * 16);
                 }
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const uint32_t b0 = u4w(w[i >> 1], 2 * (i & 1)), b1 = u4w(w[i >> 1], 2 * (i & 1) + 1);
-                    if (SPLIT) {
-                        mma_e4m3(sc[j], qh[0][2 * i], ql[0][2 * i], qh[0][2 * i + 1], ql[0][2 * i + 1], b0, b1);
-                    } else {
-                        mma_e4m3(sc[j], qh[0][2 * i], qh[1][2 * i], qh[0][2 * i + 1], qh[1][2 * i + 1], b0, b1);
-                        mma_e4m3(sc[j], ql[0][2 * i], ql[1][2 * i], ql[0][2 * i + 1], ql[1][2 * i + 1], b0, b1);
+                for (int y = 0; y < 2; ++y) {
+                    const int a = 4 * i + 2 * y;  // q's words of this K step: a, a + 1
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (SPLIT)
+                            mma_e4m3(sc[j], qh[0][a], ql[0][a], qh[0][a + 1], ql[0][a + 1], u4w(w[j], 2 * y), u4w(w[j], 2 * y + 1));
+                        else
+                            mma_e4m3(sc[j], qh[0][a], qh[1][a], qh[0][a + 1], qh[1][a + 1], u4w(w[j], 2 * y), u4w(w[j], 2 * y + 1));
+                    }
+                    if (!SPLIT) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mma_e4m3(sc[j], ql[0][a], ql[1][a], ql[0][a + 1], ql[1][a + 1], u4w(w[j], 2 * y), u4w(w[j], 2 * y + 1));
                     }
                 }
             }
@@ -507,16 +517,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                     digits4<SPLIT ? kLoShift : 0>(sc[2 * i][2 * x], sc[2 * i][2 * x + 1], sc[2 * i + 1][2 * x],
                                                   sc[2 * i + 1][2 * x + 1], ph[x][i], pl[x][i]);
 #pragma unroll
-            for (int i = 0; i < DT; ++i) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(vp + (8 * i + g) * kPage + 16 * t4);
-                if (SPLIT) {
-                    mma_e4m3(o[i], ph[0][0], pl[0][0], ph[0][1], pl[0][1], w.x, w.y);
-                    mma_e4m3(o[i], ph[0][2], pl[0][2], ph[0][3], pl[0][3], w.z, w.w);
-                } else {
-                    mma_e4m3(o[i], ph[0][0], ph[1][0], ph[0][1], ph[1][1], w.x, w.y);
-                    mma_e4m3(o[i], pl[0][0], pl[1][0], pl[0][1], pl[1][1], w.x, w.y);
-                    mma_e4m3(o[i], ph[0][2], ph[1][2], ph[0][3], ph[1][3], w.z, w.w);
-                    mma_e4m3(o[i], pl[0][2], pl[1][2], pl[0][3], pl[1][3], w.z, w.w);
+            for (int i0 = 0; i0 < DT; i0 += 8) {
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = *reinterpret_cast<const uint4 *>(vp + (8 * (i0 + i) + g) * kPage + 16 * t4);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (SPLIT)
+                            mma_e4m3(o[i0 + i], ph[0][2 * y], pl[0][2 * y], ph[0][2 * y + 1], pl[0][2 * y + 1],
+                                     u4w(w[i], 2 * y), u4w(w[i], 2 * y + 1));
+                        else
+                            mma_e4m3(o[i0 + i], ph[0][2 * y], ph[1][2 * y], ph[0][2 * y + 1], ph[1][2 * y + 1],
+                                     u4w(w[i], 2 * y), u4w(w[i], 2 * y + 1));
+                    }
+                    if (!SPLIT) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mma_e4m3(o[i0 + i], pl[0][2 * y], pl[1][2 * y], pl[0][2 * y + 1], pl[1][2 * y + 1],
+                                     u4w(w[i], 2 * y), u4w(w[i], 2 * y + 1));
+                    }
                 }
             }
             __syncwarp();

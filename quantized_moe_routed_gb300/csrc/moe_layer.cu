@@ -33,15 +33,25 @@ struct Device {
     int ordinal, sms, optin;
 };
 
-// The device (-1: the current one), which has to be sm_103.
+// The device (-1: the current one), which has to be sm_103.  Attributes do not
+// change, so each device is asked once.
 moe_status_t query_device(int dev, Device *out)
 {
+    constexpr int kKnown = 16;
+    static std::mutex mu;
+    static Device known[kKnown];
+    static bool have[kKnown];
     cudaError_t e = cudaSuccess;
     if (dev < 0) e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < kKnown && have[dev]) {
+        *out = known[dev];
+        return MOE_OK;
+    }
     int major = 0, minor = 0;
     out->ordinal = dev;
-    if (e != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&out->sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+    if ((e = cudaDeviceGetAttribute(&out->sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&out->optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess)
@@ -49,6 +59,10 @@ moe_status_t query_device(int dev, Device *out)
     if (major != 10 || minor != 3)
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "device %d is sm_%d%d; this library is built for sm_103a only", dev,
                     major, minor);
+    if (dev < kKnown) {
+        known[dev] = *out;
+        have[dev] = true;
+    }
     return MOE_OK;
 }
 

@@ -16,10 +16,11 @@ import math
 import torch
 
 from . import binding
-from .binding import MOE_ERR_INVALID_ARG, MoeError, _check, _need, _ptr, _stream
+from .binding import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _need
 
 PAGE = 64        # tokens of a cache page
 MAX_SEQS = 512   # sequences of a step
+_BF16 = (torch.bfloat16,)
 
 _P, _I, _S, _L, _F = C.c_void_p, C.c_int, C.c_size_t, C.c_int64, C.c_float
 
@@ -66,31 +67,49 @@ def _bad(msg):
     return MoeError(MOE_ERR_INVALID_ARG, msg)
 
 
-def _need_rows(t, dtypes, shape, name):
-    """A CUDA tensor whose rows are contiguous; returns its row stride in
-    elements.  Only dimension 0 may be strided."""
+# The checks below run on every call, so they compare in one go and look for the
+# reason only where that fails.
+def _rows(t, dtypes, tail, name, n=None):
+    """Row stride, in elements, of a CUDA tensor [n, *tail] whose rows are
+    contiguous (only dimension 0 may be strided)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise _bad(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise _bad(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != d for s, d in zip(shape, t.shape)):
-        raise _bad(f"{name} {tuple(t.shape)} is not {['any' if s is None else s for s in shape]}")
-    row = 1
-    for d in range(t.dim() - 1, 0, -1):
-        if t.shape[d] != 1 and t.stride(d) != row:
-            raise _bad(f"a row of {name} must be contiguous (strides {t.stride()})")
-        row *= t.shape[d]
-    return t.stride(0) if t.shape[0] > 1 else max(row, 1)
+    shape = t.shape
+    if len(shape) != len(tail) + 1 or shape[1:] != tail or (n is not None and shape[0] != n):
+        raise _bad(f"{name} {tuple(shape)} is not {('T' if n is None else n, *tail)}")
+    stride, row = t.stride(), 1
+    for d in range(len(tail), 0, -1):
+        if stride[d] != row and shape[d] != 1:
+            raise _bad(f"a row of {name} must be contiguous (strides {stride})")
+        row *= shape[d]
+    return stride[0] if shape[0] > 1 else max(row, 1)
 
 
 def _need_out(t, dtype, shape, device, name):
-    _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape) or t.device != device:
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and
+            t.is_contiguous()):
+        _need(t, dtype, name)
         raise _bad(f"{name} {tuple(t.shape)} on {t.device} is not {tuple(shape)} on {device}")
 
 
-def _on(stream, device):
-    return torch.cuda.current_stream(device) if stream is None else stream
+def _empty(shape, dtype, device, stream):
+    """Allocated on the stream that the call runs on, so that its memory is not
+    handed out again while the work queued there may still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _handle(stream, device):
+    """cudaStream_t of `stream`, or of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _same_device(device, **tensors):
@@ -109,8 +128,10 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, residual_out=None,
     [T, H / 128]), "both" returns (y, codes, scales)."""
     if outputs not in ("bf16", "e4m3", "both"):
         raise _bad(f"outputs={outputs!r} is not bf16, e4m3 or both")
-    stride = _need_rows(x, (torch.float32, torch.bfloat16), (None, None), "x")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise _bad("x must be a CUDA tensor [T, H]")
     T, H = x.shape
+    stride = _rows(x, (torch.float32, torch.bfloat16), (H,), "x")
     dev = x.device
     _need_out(weight, torch.bfloat16, (H,), dev, "weight")
     if residual is None:
@@ -120,28 +141,30 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, residual_out=None,
         _need_out(residual, torch.bfloat16, (T, H), dev, "residual")
         if residual_out is None:
             residual_out = residual
-        _need_out(residual_out, torch.bfloat16, (T, H), dev, "residual_out")
-    st = _on(stream, dev)
-    quant = outputs != "bf16"
-    with torch.cuda.stream(st):
-        if outputs != "e4m3" and out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        if quant and out_q is None:
-            out_q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
-        if quant and out_scale is None:
-            out_scale = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+        else:
+            _need_out(residual_out, torch.bfloat16, (T, H), dev, "residual_out")
     if outputs == "e4m3":
         if out is not None:
             raise _bad("out with outputs='e4m3'")
+    elif out is None:
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     else:
         _need_out(out, torch.bfloat16, (T, H), dev, "out")
-    if quant:
+    if outputs == "bf16":
+        if out_q is not None or out_scale is not None:
+            raise _bad("out_q or out_scale with outputs='bf16'")
+    else:
+        if out_q is None:
+            out_q = _empty((T, H), torch.float8_e4m3fn, dev, stream)
+        if out_scale is None:
+            out_scale = _empty((T, H // 128), torch.float32, dev, stream)
         _need_out(out_q, torch.float8_e4m3fn, (T, H), dev, "out_q")
         _need_out(out_scale, torch.float32, (T, H // 128), dev, "out_scale")
-    elif out_q is not None or out_scale is not None:
-        raise _bad("out_q or out_scale with outputs='bf16'")
-    _check(_library().moe_norm(_ptr(x), int(x.dtype == torch.float32), stride, _ptr(residual), _ptr(residual_out),
-                               _ptr(weight), eps, _ptr(out), _ptr(out_q), _ptr(out_scale), T, H, _stream(st)))
+    st = _library().moe_norm(x.data_ptr(), x.dtype == torch.float32, stride, _ptr(residual), _ptr(residual_out),
+                             weight.data_ptr(), eps, _ptr(out), _ptr(out_q), _ptr(out_scale), T, H,
+                             _handle(stream, dev))
+    if st != MOE_OK:
+        _check(st)
     return out if outputs == "bf16" else ((out_q, out_scale) if outputs == "e4m3" else (out, out_q, out_scale))
 
 
@@ -162,22 +185,27 @@ class Nvfp4Linear:
         self.q, self.s = q, s
         self.ts = ts.expand(q.shape[0]).contiguous()
         self.N, self.K = q.shape[0], 2 * q.shape[1]
+        self._weights = (q.data_ptr(), s.data_ptr(), self.ts.data_ptr(), self.N, self.K)
 
     def __call__(self, x, dtype=torch.float32, out=None, stream=None):
         """x bfloat16 [T, K] (rows may be strided) -> [T, N] float32 or bfloat16."""
-        stride = _need_rows(x, (torch.bfloat16,), (None, self.K), "x")
-        _same_device(self.q.device, x=x)
+        dev = self.q.device
+        stride = _rows(x, _BF16, (self.K,), "x")
+        if x.device != dev:
+            _same_device(dev, x=x)
+        T = x.shape[0]
         if out is not None:
             dtype = out.dtype
         if dtype not in (torch.float32, torch.bfloat16):
             raise _bad(f"dtype {dtype} is not float32 or bfloat16")
-        st = _on(stream, x.device)
         if out is None:
-            with torch.cuda.stream(st):
-                out = torch.empty((x.shape[0], self.N), dtype=dtype, device=x.device)
-        _need_out(out, dtype, (x.shape[0], self.N), x.device, "out")
-        _check(_library().moe_linear(_ptr(self.q), _ptr(self.s), _ptr(self.ts), self.N, self.K, _ptr(x), stride,
-                                     _ptr(out), int(dtype == torch.bfloat16), x.shape[0], _stream(st)))
+            out = _empty((T, self.N), dtype, dev, stream)
+        else:
+            _need_out(out, dtype, (T, self.N), dev, "out")
+        st = _library().moe_linear(*self._weights, x.data_ptr(), stride, out.data_ptr(), dtype == torch.bfloat16, T,
+                                   _handle(stream, dev))
+        if st != MOE_OK:
+            _check(st)
         return out
 
 
@@ -236,6 +264,9 @@ class KVCache:
                         None if rope is None else rope.data_ptr(), dev.index)
         self.handle = C.c_void_p()
         _check(_library().moe_kv_create(C.byref(d), C.byref(self.handle)))
+        self._ws_bytes = int(_library().moe_kv_workspace_bytes(self.handle))
+        self._q_row, self._kv_row = (q_heads, head_dim), (kv_heads, head_dim)
+        self._scale = 1.0 / math.sqrt(head_dim)
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -245,73 +276,79 @@ class KVCache:
 
     def new_workspace(self, stream=None) -> torch.Tensor:
         """Zeroed workspace for append and attend: one per concurrent stream."""
-        n = int(_library().moe_kv_workspace_bytes(self.handle))
-        st = _on(stream, self.device)
-        with torch.cuda.stream(st):
-            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        _check(_library().moe_kv_workspace_init(self.handle, _ptr(ws), n, _stream(st)))
+        ws = _empty((self._ws_bytes,), torch.uint8, self.device, stream)
+        _check(_library().moe_kv_workspace_init(self.handle, ws.data_ptr(), self._ws_bytes, _handle(stream, self.device)))
         return ws
 
-    def _batch(self, q_off, kv_len, pages, N, max_q):
+    def _step(self, q_off, kv_len, pages, ws, N, max_q):
+        """The batch description; checks the step's arrays and the workspace."""
+        B = kv_len.shape[0] if isinstance(kv_len, torch.Tensor) and kv_len.dim() == 1 else -1
         for name, t in (("q_off", q_off), ("kv_len", kv_len), ("pages", pages)):
-            _need(t, torch.int32, name)
-            _same_device(self.device, **{name: t})
-        B = kv_len.shape[0] if kv_len.dim() == 1 else -1
-        if B < 0 or tuple(q_off.shape) != (B + 1,) or pages.dim() != 2 or pages.shape[0] != B:
+            if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == self.device and
+                    t.is_contiguous()):
+                _need(t, torch.int32, name)
+                _same_device(self.device, **{name: t})
+        if B < 0 or q_off.shape != (B + 1,) or pages.dim() != 2 or pages.shape[0] != B:
             raise _bad(f"shapes q_off {tuple(q_off.shape)}, kv_len {tuple(kv_len.shape)}, pages {tuple(pages.shape)} "
                        "are not [B + 1], [B], [B, max_pages]")
-        return moe_kv_batch(q_off.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, N, max_q)
+        self._need_ws(ws)
+        return C.byref(moe_kv_batch(q_off.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, N, max_q))
 
     def _need_ws(self, ws):
-        _need(ws, torch.uint8, "ws")
-        _same_device(self.device, ws=ws)
-        if ws.numel() < int(_library().moe_kv_workspace_bytes(self.handle)):
+        if not (isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.device == self.device and
+                ws.is_contiguous() and ws.numel() >= self._ws_bytes):
+            _need(ws, torch.uint8, "ws")
+            _same_device(self.device, ws=ws)
             raise _bad("ws is smaller than this cache's workspace (new_workspace)")
 
     def append(self, k, v, q_off, kv_len, pages, ws, max_q: int, q=None, q_out=None, stream=None):
         """Rotate and append the new tokens' k and v (bfloat16 [N, kv_heads,
         head_dim], tokens may be strided), and rotate q (bfloat16 [N, q_heads,
         head_dim]) into q_out, which is returned (None without q)."""
-        ks = _need_rows(k, (torch.bfloat16,), (None, self.kv_heads, self.head_dim), "k")
+        dev = self.device
+        ks = _rows(k, _BF16, self._kv_row, "k")
         N = k.shape[0]
-        vs = _need_rows(v, (torch.bfloat16,), (N, self.kv_heads, self.head_dim), "v")
-        _same_device(self.device, k=k, v=v)
+        vs = _rows(v, _BF16, self._kv_row, "v", N)
         qs = 0
-        st = _on(stream, self.device)
+        if k.device != dev or v.device != dev:
+            _same_device(dev, k=k, v=v)
         if q is not None:
-            qs = _need_rows(q, (torch.bfloat16,), (N, self.q_heads, self.head_dim), "q")
-            _same_device(self.device, q=q)
+            qs = _rows(q, _BF16, self._q_row, "q", N)
+            if q.device != dev:
+                _same_device(dev, q=q)
             if q_out is None:
-                with torch.cuda.stream(st):
-                    q_out = torch.empty((N, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
-            _need_out(q_out, torch.bfloat16, (N, self.q_heads, self.head_dim), self.device, "q_out")
+                q_out = _empty((N, *self._q_row), torch.bfloat16, dev, stream)
+            else:
+                _need_out(q_out, torch.bfloat16, (N, *self._q_row), dev, "q_out")
         elif q_out is not None:
             raise _bad("q_out without q")
-        self._need_ws(ws)
-        batch = self._batch(q_off, kv_len, pages, N, max_q)
-        _check(_library().moe_kv_append(self.handle, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_out),
-                                        C.byref(batch), _ptr(ws), _stream(st)))
+        st = _library().moe_kv_append(self.handle, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_out),
+                                      self._step(q_off, kv_len, pages, ws, N, max_q), ws.data_ptr(),
+                                      _handle(stream, dev))
+        if st != MOE_OK:
+            _check(st)
         return q_out
 
     def attend(self, q, q_off, kv_len, pages, ws, max_q: int, scale: float = None, out=None, stream=None):
         """Causal attention of q (bfloat16 [N, q_heads, head_dim], tokens may be
         strided) over the cache: bfloat16 [N, q_heads, head_dim].  scale: 1 /
         sqrt(head_dim) unless given."""
-        qs = _need_rows(q, (torch.bfloat16,), (None, self.q_heads, self.head_dim), "q")
-        _same_device(self.device, q=q)
-        st = _on(stream, self.device)
+        dev = self.device
+        qs = _rows(q, _BF16, self._q_row, "q")
+        if q.device != dev:
+            _same_device(dev, q=q)
         if out is None:
-            with torch.cuda.stream(st):
-                out = torch.empty((q.shape[0], self.q_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
-        _need_out(out, torch.bfloat16, (q.shape[0], self.q_heads, self.head_dim), self.device, "out")
-        self._need_ws(ws)
-        batch = self._batch(q_off, kv_len, pages, q.shape[0], max_q)
-        _check(_library().moe_kv_attend(self.handle, _ptr(q), qs,
-                                        1.0 / math.sqrt(self.head_dim) if scale is None else scale, _ptr(out),
-                                        C.byref(batch), _ptr(ws), _stream(st)))
+            out = _empty(q.shape, torch.bfloat16, dev, stream)
+        else:
+            _need_out(out, torch.bfloat16, q.shape, dev, "out")
+        st = _library().moe_kv_attend(self.handle, q.data_ptr(), qs, self._scale if scale is None else scale,
+                                      out.data_ptr(), self._step(q_off, kv_len, pages, ws, q.shape[0], max_q),
+                                      ws.data_ptr(), _handle(stream, dev))
+        if st != MOE_OK:
+            _check(st)
         return out
 
     def check(self, ws, stream=None) -> int:
         """Synchronise and return the device status (0 = MOE_OK); clears it."""
         self._need_ws(ws)
-        return int(_library().moe_kv_check(self.handle, _ptr(ws), _stream(_on(stream, self.device))))
+        return int(_library().moe_kv_check(self.handle, ws.data_ptr(), _handle(stream, self.device)))
