@@ -175,14 +175,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-CUresult encode_rows(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, int box_c, int box_r, bool sw128)
+CUresult encode_rows(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, int box_c, int box_r, int swizzle)
 {
     const cuuint32_t es[2] = {1, 1};
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_c), static_cast<cuuint32_t>(box_r)};
     return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     sw128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                     : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
@@ -665,10 +667,10 @@ moe_status_t run_tc(moe_plan *pl, const void *x, const int32_t *ids, const float
         }
         p.xtok = xtok ? 1 : 0;
         const uint64_t xrows = p.xtok ? static_cast<uint64_t>(4 * Tn) : static_cast<uint64_t>(pl->tc_rows);
-        CUresult cr = encode_rows(&p.tmt[6], p.xq, xrows, d.H / 2, 128, NA, true);
-        if (cr == CUDA_SUCCESS) cr = encode_rows(&p.tmt[7], p.xsf, xrows, d.H / 16, 16, NA, false);
-        if (cr == CUDA_SUCCESS) cr = encode_rows(&p.tmt[8], p.hq, pl->tc_rows, pl->Ipad / 2, 128, N, true);
-        if (cr == CUDA_SUCCESS) cr = encode_rows(&p.tmt[9], p.hsf, pl->tc_rows, pl->Ipad / 16, 16, N, false);
+        CUresult cr = encode_rows(&p.tmt[6], p.xq, xrows, d.H / 2, 128, NA, 128);
+        if (cr == CUDA_SUCCESS) cr = encode_rows(&p.tmt[7], p.xsf, xrows, d.H / 16, 16, NA, 0);
+        if (cr == CUDA_SUCCESS) cr = encode_rows(&p.tmt[8], p.hq, pl->tc_rows, pl->Ipad / 2, 128, N, 128);
+        if (cr == CUDA_SUCCESS) cr = encode_rows(&p.tmt[9], p.hsf, pl->tc_rows, pl->Ipad / 16, 16, N, 0);
         if (cr != CUDA_SUCCESS) {
             reject(pl);
             return fail(MOE_ERR_CUDA, "tensor-map encoding of the workspace failed (CUresult %d)", static_cast<int>(cr));

@@ -20,9 +20,9 @@ inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_
 // cuTensorMapEncodeTiled from the driver, or null where it is not available.
 PFN_cuTensorMapEncodeTiled_v12000 encoder();
 
-// Row-major uint8 [rows, cols] with a {box_c, box_r} box, with or without the
-// 128-byte swizzle.
-CUresult encode_rows(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, int box_c, int box_r, bool sw128);
+// Row-major uint8 [rows, cols] with a {box_c, box_r} box, swizzled over 128 or 64
+// bytes (0: not).
+CUresult encode_rows(CUtensorMap *m, void *base, uint64_t rows, uint64_t cols, int box_c, int box_r, int swizzle);
 
 // Limit of a device-side wait: 1 s, or MOE_WAIT_TIMEOUT_MS.
 long long wait_limit_ns();

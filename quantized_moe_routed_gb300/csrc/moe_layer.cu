@@ -18,7 +18,7 @@ struct moe_kv {
     moe_kv_desc d;
     int device = 0, num_sms = 0, smem_optin = 0;
     long long timeout_ns = 0;
-    CUtensorMap tm_k{};
+    CUtensorMap tm_k{}, tm_v{};
     size_t off_count = 0, off_part = 0, ws_bytes = 0;
 };
 
@@ -108,7 +108,7 @@ moe::KvParams kv_params(const moe_kv *kv, const moe_kv_batch *b, void *ws)
 {
     moe::KvParams c{};
     const moe_kv_desc &d = kv->d;
-    c.tm_k = kv->tm_k;
+    c.tm_k = kv->tm_k, c.tm_v = kv->tm_v;
     c.k = d.k_dev, c.v = d.v_dev, c.ks = d.k_scale_dev, c.vs = d.v_scale_dev, c.rope = d.rope_dev;
     c.n_pages = d.n_pages, c.q_heads = d.q_heads, c.kv_heads = d.kv_heads, c.D = d.head_dim;
     c.rot_dim = d.rot_dim, c.rot_inter = d.rot_interleaved, c.rope_positions = d.rope_positions;
@@ -117,6 +117,11 @@ moe::KvParams kv_params(const moe_kv *kv, const moe_kv_batch *b, void *ws)
     c.ctrl = static_cast<uint32_t *>(ws);
     return c;
 }
+
+// Query rows of a tile of the attention, from the rows of the sequence with the
+// most new tokens: up to 16 the kernel of few rows, whose warps share no rows;
+// above, the tensor-memory kernel, whose rows come by 128.
+int attend_tile_rows(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 128 ? 128 : 256)); }
 
 }  // namespace
 
@@ -207,14 +212,12 @@ moe_status_t moe_kv_create(const moe_kv_desc *desc, moe_kv_t *out)
     kv->num_sms = dev.sms;
     kv->smem_optin = dev.optin;
     kv->timeout_ns = moe::wait_limit_ns();
-    if (d.head_dim == 128) {
-        const CUresult r = moe::encode_rows(&kv->tm_k, d.k_dev,
-                                            static_cast<uint64_t>(d.n_pages) * d.kv_heads * MOE_KV_PAGE, 128, 128,
-                                            MOE_KV_PAGE, true);
-        if (r != CUDA_SUCCESS) {
-            delete kv;
-            return fail(MOE_ERR_CUDA, "tensor-map encoding failed (CUresult %d)", static_cast<int>(r));
-        }
+    const uint64_t ph = static_cast<uint64_t>(d.n_pages) * d.kv_heads;
+    CUresult r = moe::encode_rows(&kv->tm_k, d.k_dev, ph * MOE_KV_PAGE, d.head_dim, d.head_dim, MOE_KV_PAGE, d.head_dim);
+    if (r == CUDA_SUCCESS) r = moe::encode_rows(&kv->tm_v, d.v_dev, ph * d.head_dim, MOE_KV_PAGE, MOE_KV_PAGE, d.head_dim, MOE_KV_PAGE);
+    if (r != CUDA_SUCCESS) {
+        delete kv;
+        return fail(MOE_ERR_CUDA, "tensor-map encoding failed (CUresult %d)", static_cast<int>(r));
     }
     kv->off_count = moe::kCtrlBytes;
     kv->off_part = kv->off_count + (static_cast<size_t>(dev.sms) * 4 + 255) / 256 * 256;
@@ -276,10 +279,10 @@ moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, flo
     if ((st = check_rows(q_dev, q_stride, static_cast<int64_t>(kv->d.q_heads) * kv->d.head_dim, "q")) != MOE_OK) return st;
     if (!o_dev) return fail(MOE_ERR_INVALID_ARG, "null o pointer");
     if (!aligned(o_dev, 16)) return fail(MOE_ERR_MISALIGNED, "o needs 16-byte alignment");
-    // the kernel counts the units of a sequence (pages of all its tiles) in 32 bits
     const long long G = kv->d.q_heads / kv->d.kv_heads;
-    const long long tiles = batch->N * G / moe::attend_tile_rows(batch->max_q * G) + 1;
-    if (tiles > 0x7FFFFFFFLL / kv->d.kv_heads / batch->max_pages)
+    const int tile_rows = attend_tile_rows(batch->max_q * G);
+    // the kernels count the units of a sequence (pages of all its tiles) in 32 bits
+    if (batch->N * G / tile_rows + 1 > 0x7FFFFFFFLL / kv->d.kv_heads / batch->max_pages)
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "N=%d new tokens over max_pages=%d pages are too many for one step", batch->N,
                     batch->max_pages);
     uint8_t *ws = static_cast<uint8_t *>(ws_dev);
@@ -288,7 +291,8 @@ moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, flo
                         reinterpret_cast<float *>(ws + kv->off_part), kv->timeout_ns};
     moe::WsTicket tk;
     if ((st = moe::ws_claim(ws_dev, static_cast<cudaStream_t>(stream), tk)) != MOE_OK) return st;
-    const cudaError_t e = moe::launch_kv_attend(p, kv->num_sms, kv->smem_optin, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = (tile_rows <= 16 ? moe::launch_kv_attend_rows : moe::launch_kv_attend_tc)(
+        p, tile_rows, kv->num_sms, kv->smem_optin, static_cast<cudaStream_t>(stream));
     moe::ws_release(tk, e == cudaSuccess);
     return launched(e, "attention launch");
 }

@@ -39,7 +39,9 @@ cudaError_t launch_linear(const LinearParams &p, int num_sms, cudaStream_t st);
 
 // The cache's pages, and one step's sequences (fields as in moe_layer.h).
 struct KvParams {
-    CUtensorMap tm_k;  // head_dim 128: k as rows of 128 bytes, box {128, 64}, 128-byte swizzle
+    // a page's k as 64 rows of head_dim bytes, its v as head_dim rows of 64,
+    // swizzled by the row's length (128 or 64 bytes)
+    CUtensorMap tm_k, tm_v;
     uint8_t *k, *v;
     float *ks, *vs;
     const float *rope;
@@ -60,7 +62,7 @@ struct AppendParams {
 };
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t st);
 
-// moe_kv_attend.cu
+// moe_kv_attend.cu: tiles of 8 or 16 rows
 struct AttendParams {
     KvParams c;
     const uint16_t *q;
@@ -68,15 +70,13 @@ struct AttendParams {
     long long q_stride;
     float scale_log2;   // softmax scale times log2(e)
     uint32_t *count;    // [grid] arrivals at the tiles that start in a CTA and end in a later one
-    float *part;        // [2 * grid] partial results (kPartFloats each)
+    float *part;        // [2 * grid] partial results (attend_part_floats each)
     long long timeout_ns;
 };
-constexpr int kAttendMaxRows = 128;  // query rows of the largest tile
-inline size_t attend_part_floats(int D) { return static_cast<size_t>(kAttendMaxRows) * (D + 2); }
-// Query rows of a tile: the smallest that holds the rows of a sequence's longest
-// run of new tokens (more rows share a page's codes, more page groups keep a
-// block's warps busy when there are few rows).
-int attend_tile_rows(long long rows);
-cudaError_t launch_kv_attend(const AttendParams &p, int num_sms, int smem_optin, cudaStream_t st);
+constexpr int kAttendMaxRows = 256;  // query rows of the largest tile
+__host__ __device__ inline size_t attend_part_floats(int D) { return static_cast<size_t>(kAttendMaxRows) * (D + 2); }
+cudaError_t launch_kv_attend_rows(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st);
+// moe_kv_attend_tc.cu: tiles of 128 or 256 rows
+cudaError_t launch_kv_attend_tc(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st);
 
 }  // namespace moe
