@@ -13,11 +13,6 @@
 #pragma once
 
 constexpr int kPage = MOE_KV_PAGE;
-constexpr int kConsumers = 256;
-constexpr int kThreads = kConsumers + 128;  // consumers, and a warpgroup with the producer
-// Registers a thread of the two kinds keeps: 256 * 216 + 128 * 72 = 64512, what
-// the block is launched with (384 threads of 168).
-constexpr int kConsumerRegs = 216, kProducerRegs = 72;
 constexpr int kMaxStages = 12;
 
 // What a block knows of every sequence.
@@ -62,7 +57,7 @@ __device__ __forceinline__ void plan_units(const AttendParams &p, Seqs &sq, int 
 {
     const KvParams &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    for (int b = tid; b < c.B; b += kThreads) {
+    for (int b = tid; b < c.B; b += blockDim.x) {
         const int a0 = c.q_off[b], a1 = c.q_off[b + 1], l = c.kv_len[b];
         const int q0 = min(max(a0, 0), c.N), q1 = min(max(a1, q0), c.N);
         const int len = l < 0 || l > c.max_pages * kPage ? 0 : l;  // out of range: nothing is seen
@@ -74,7 +69,7 @@ __device__ __forceinline__ void plan_units(const AttendParams &p, Seqs &sq, int 
         sq.per_head[b] = rows == 0 ? 0 : (rows <= TR ? tile_units(len, q1 - q0, G, TR, 0) : -1);
     }
     __syncthreads();
-    for (int b = wid; b < c.B; b += kThreads / 32) {  // sequences of several tiles: a warp each
+    for (int b = wid; b < c.B; b += blockDim.x >> 5) {  // sequences of several tiles: a warp each
         if (sq.per_head[b] >= 0) continue;
         const int n = sq.n[b], len = sq.len[b], tiles = (n * G + TR - 1) / TR;
         int sum = 0;
@@ -190,40 +185,89 @@ __device__ __forceinline__ float *part_slot(const AttendParams &p, int block, bo
 }
 
 // A tile cut between blocks: the last of them to arrive joins the partials of
-// all and writes the output.  The 256 consumers; their partials are written.
-template <int D>
+// all and writes the output.  NT consumers (the block's first), their partials
+// written.
+template <int D, int NT>
 __device__ __forceinline__ void join_tile(const AttendParams &p, const Segment &s, long long U, int blocks, int TR,
                                           int rows, int q0, int G, float gain, int *last)
 {
     const int tid = threadIdx.x;
     const int c0 = block_of(U, blocks, s.start), c1 = block_of(U, blocks, s.start + s.units - 1);
     __threadfence();
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
     if (tid == 0) {
         const uint32_t old = atom_add_acqrel_gpu(p.count + c0, 1u);
         *last = old == static_cast<uint32_t>(c1 - c0);
         if (*last) p.count[c0] = 0u;
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
     if (!*last) return;
     __threadfence();
-    for (int i = tid; i < TR * (D / 2); i += kConsumers) {
-        const int rr = i / (D / 2), d = 2 * (i % (D / 2)), r = s.tile * TR + rr;
-        if (r >= rows) break;
-        float mv = -INFINITY, lv = 0.f, a = 0.f, b = 0.f;
-        for (int k = c0; k <= c1; ++k) {
-            const float *q = part_slot(p, k, k == c0);
-            const float mk = __ldcg(q + rr), lk = __ldcg(q + TR + rr);
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(q + 2 * TR + rr * D + d));
-            const float mn = fmaxf(mv, mk), ref = mn == -INFINITY ? 0.f : mn;
-            const float f0 = ex2(mv - ref), f1 = ex2(mk - ref);
-            lv = lv * f0 + lk * f1;
-            a = a * f0 + v.x * f1;
-            b = b * f0 + v.y * f1;
-            mv = mn;
+    // a warp takes RU rows at a time (their loads in flight together); a lane
+    // holds one block's factor, and D / 32 columns of the sums
+    constexpr int RU = 4, V = D / 32;
+    const int lane = tid & 31, mine = min(TR, rows - s.tile * TR);
+    for (int r0 = (tid >> 5) * RU; r0 < mine; r0 += NT / 32 * RU) {
+        float M[RU], L[RU], acc[RU][V];
+#pragma unroll
+        for (int i = 0; i < RU; ++i) {
+            M[i] = -INFINITY;
+            L[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[i][j] = 0.f;
         }
-        const float inv = inv_sum(gain, lv);
-        *reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, r) + d) = pack_bf16(a * inv, b * inv);
+        for (int k0 = c0; k0 <= c1; k0 += 32) {  // 32 blocks at a time
+            const int kk = k0 + lane;
+            const float *q = part_slot(p, min(kk, c1), min(kk, c1) == c0);
+            float f[RU], lk[RU];
+#pragma unroll
+            for (int i = 0; i < RU; ++i) {
+                const int rr = min(r0 + i, mine - 1);
+                f[i] = kk <= c1 ? __ldcg(q + rr) : -INFINITY;
+                lk[i] = kk <= c1 ? __ldcg(q + TR + rr) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < RU; ++i) {
+                float m = f[i];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                m = fmaxf(m, M[i]);
+                const float ref = m == -INFINITY ? 0.f : m, back = ex2(M[i] - ref);
+                f[i] = ex2(f[i] - ref);
+                float l = lk[i] * f[i];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                L[i] = L[i] * back + l;
+                M[i] = m;
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[i][j] *= back;
+            }
+            const int m = min(32, c1 - k0 + 1);
+#pragma unroll 4
+            for (int k = 0; k < m; ++k) {
+                const float *o = part_slot(p, k0 + k, k0 + k == c0) + 2 * TR + V * lane;
+#pragma unroll
+                for (int i = 0; i < RU; ++i) {
+                    const float *v = o + static_cast<size_t>(min(r0 + i, mine - 1)) * D;
+                    const float fk = __shfl_sync(0xffffffffu, f[i], k);
+                    if (V == 4) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(v));
+                        acc[i][0] += x.x * fk, acc[i][1] += x.y * fk, acc[i][2] += x.z * fk, acc[i][V - 1] += x.w * fk;
+                    } else {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
+                        acc[i][0] += x.x * fk, acc[i][1] += x.y * fk;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RU; ++i) {
+            if (r0 + i >= mine) break;
+            const float inv = inv_sum(gain, L[i]);
+            uint32_t *o = reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, s.tile * TR + r0 + i) + V * lane);
+#pragma unroll
+            for (int j = 0; j < V; j += 2) o[j / 2] = pack_bf16(acc[i][j] * inv, acc[i][j + 1] * inv);
+        }
     }
 }
 

@@ -40,7 +40,12 @@ namespace {
 
 #include "moe_attend.cuh"
 
-constexpr int kWarps = kConsumers / 32;
+constexpr int kWarps = 8;
+constexpr int kConsumers = kWarps * 32;
+constexpr int kThreads = kConsumers + 128;  // consumers, and a warpgroup whose first warp is the producer
+// Registers a thread of the two kinds keeps: 256 * 216 + 128 * 72 = 64512, what
+// the block is launched with (384 threads of 168).
+constexpr int kConsumerRegs = 216, kProducerRegs = 72;
 
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 *reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, r) + d) = pack_bf16(a * inv, b * inv);
             }
         }
-        if (!s.whole()) join_tile<D>(p, s, U, blocks, TR, rows, q0, G, 256.f, &ct->last);
+        if (!s.whole()) join_tile<D, kConsumers>(p, s, U, blocks, TR, rows, q0, G, 256.f, &ct->last);
     }
 }
 

@@ -21,12 +21,12 @@
 // log2(vs)), moved only when a tile exceeds it by more than 2 (the digits hold
 // four times the usual largest), so the accumulators in tensor memory are rescaled rarely.
 //
-// A block runs two streams, each with a warpgroup for the softmax (a thread a
-// row) and its own S / P and O in tensor memory, so that one stream's softmax
-// and the other's products overlap.  With TWO, the streams are two row tiles
+// A block runs two streams, each with two warpgroups for the softmax (two
+// threads a row, each a page of the stage) and its own S / P and O in tensor memory, so that
+// one stream's softmax and the other's products overlap.  With TWO, the streams are two row tiles
 // that share the pages; otherwise they are the even and the odd page pairs of
-// one row tile, joined at the end.  One warp brings pages (two a stage), one thread
-// issues the MMAs.
+// one row tile, joined at the end.  One warp brings pages (two a stage), one thread a
+// stream issues the MMAs.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -44,6 +44,12 @@ namespace {
 
 #include "moe_attend.cuh"
 
+constexpr int kStream = 256;     // softmax threads of a stream
+constexpr int kConsumers = 2 * kStream;
+constexpr int kThreads = kConsumers + 128;  // and a warpgroup with the producer and the MMA issuers
+// Registers a thread of the two kinds keeps: 512 * 104 + 128 * 48 = 59392, within
+// what the block is launched with (640 threads of 96).
+constexpr int kConsumerRegs = 104, kProducerRegs = 48;
 constexpr int kRows = 128;       // rows of a stream: tensor-memory lanes
 constexpr int kKeys = 2 * kPage; // tokens of a stage
 constexpr float kGain = 64.f;    // of the weights' digits
@@ -52,10 +58,11 @@ constexpr int kTmemCols = 512;   // stream s: S / P at 256 s, O at 256 s + 128
 
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_ready, s_ready[2], p_ready[2], o_ready[2], drained;
+    uint64_t q_ready, s_ready[2], p_ready[2], o_ready[2], drained[2];
     float ks[kMaxStages][2], vs[kMaxStages][2];  // scales of the stage's pages; ks < 0: no such page
     float qs[2][kRows];                          // each row's factor from digits to scores (log2 units)
-    float m[2][kRows], l[2][kRows];              // the streams' references and sums, for joining them
+    float mx[2][2][kRows];                       // [stream][page]: largest of a row in a stage's page
+    float m[2][kRows], l[2][2][kRows];           // references, and sums of the two pages, at a tile's end
     uint32_t tmem;
     int abort, last;
 };
@@ -112,34 +119,18 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&u)[16])
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t f16x2)
-{
-    uint32_t r;
-    asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n cvt.u32.u16 %0, t;\n}" : "=r"(r) : "r"(f16x2));
-    return r;
-}
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 // Four values (at most 448 in magnitude) as two E4M3 digits: hi the nearest, lo
 // the nearest to the rest.
 __device__ __forceinline__ void digits4(float a, float b, float c, float d, uint32_t &hi, uint32_t &lo)
 {
-    const uint32_t x = cvt_f16x2(a, b), y = cvt_f16x2(c, d);
-    const uint32_t hx = cvt_e4m3x2(x), hy = cvt_e4m3x2(y);
-    const uint32_t rx = hsub2(x, e4m3x2_to_f16x2(static_cast<uint16_t>(hx)));
-    const uint32_t ry = hsub2(y, e4m3x2_to_f16x2(static_cast<uint16_t>(hy)));
-    hi = hx | (hy << 16);
-    lo = cvt_e4m3x2(rx) | (cvt_e4m3x2(ry) << 16);
+    asm("{\n .reg .b32 x, y, hx, hy;\n .reg .b16 p, q;\n"
+        " cvt.rn.f16x2.f32 x, %3, %2;\n cvt.rn.f16x2.f32 y, %5, %4;\n"
+        " cvt.rn.satfinite.e4m3x2.f16x2 p, x;\n cvt.rn.satfinite.e4m3x2.f16x2 q, y;\n mov.b32 %0, {p, q};\n"
+        " cvt.rn.f16x2.e4m3x2 hx, p;\n cvt.rn.f16x2.e4m3x2 hy, q;\n"
+        " sub.rn.f16x2 x, x, hx;\n sub.rn.f16x2 y, y, hy;\n"
+        " cvt.rn.satfinite.e4m3x2.f16x2 p, x;\n cvt.rn.satfinite.e4m3x2.f16x2 q, y;\n mov.b32 %1, {p, q};\n}"
+        : "=r"(hi), "=r"(lo)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
 // 16-byte granule gr of row `row` in a swizzled tile of D-byte rows.
@@ -152,7 +143,7 @@ __device__ __forceinline__ int granule(int row, int gr)
 // Half a query row (thread pairs share a row) as two digits into the tile at dst
 // (hi; lo follows kRows * D bytes on); returns the row's factor.
 template <int D>
-__device__ __forceinline__ float put_query(uint8_t *dst, int row, int half, const uint16_t *src, bool in, float scale_log2)
+__device__ __forceinline__ float put_query(uint8_t *dst, int row, int half, const uint16_t *src, bool in, float scale)
 {
     uint4 w[D / 16];
 #pragma unroll
@@ -165,7 +156,7 @@ __device__ __forceinline__ float put_query(uint8_t *dst, int row, int half, cons
     am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
     // largest magnitude into [128, 256)
     const int e = am < 0x0080u ? 120 : max(-120, min(120, 7 + 127 - static_cast<int>(am >> 7)));
-    const float f = exp2i(e);
+    const float f = scale < 0.f ? -exp2i(e) : exp2i(e);  // the scale's sign is in the digits
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
         uint32_t hi[4], lo[4];
@@ -179,7 +170,7 @@ __device__ __forceinline__ float put_query(uint8_t *dst, int row, int half, cons
         *reinterpret_cast<uint4 *>(o + kRows * D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     // a NaN or an infinity in the row: NaN scores
-    return am >= 0x7F80u ? __int_as_float(0x7FC00000) : exp2i(-e) * scale_log2;
+    return am >= 0x7F80u ? __int_as_float(0x7FC00000) : exp2i(-e) * fabsf(scale);
 }
 
 template <int D, bool TWO>
@@ -205,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             mbar_init(&ct->empty[i], TWO ? 2 : 1);
         }
         mbar_init(&ct->q_ready, kConsumers);
-        mbar_init(&ct->drained, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ct->s_ready[s], 1);
-            mbar_init(&ct->p_ready[s], kRows);
+            mbar_init(&ct->p_ready[s], kStream);
             mbar_init(&ct->o_ready[s], 1);
+            mbar_init(&ct->drained[s], 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -220,15 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
     if (static_cast<int>(blockIdx.x) >= blocks) return;
     const long long u0 = block_start(U, blocks, blockIdx.x), u1 = block_start(U, blocks, blockIdx.x + 1);
-    if (wid == 9) tc_alloc(&ct->tmem, kTmemCols);
+    constexpr int kProducer = kConsumers / 32, kIssuer = kProducer + 1;  // warps
+    if (wid == kIssuer) tc_alloc(&ct->tmem, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ct->tmem;
 
-    if (wid >= 8) {
+    if (wid >= kProducer) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        if (wid == 8) {
+        if (wid == kProducer) {
             // ---- producer: two pages a stage; an odd last page comes twice (the
             // second copy is behind every row's mask)
             int it = 0;
@@ -278,80 +270,69 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                            static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
                     }
             }
-        } else if (wid == 9) {
-            // ---- MMA issue: one thread (the whole warp finds the segments)
+        } else if (wid == kIssuer || wid == kIssuer + 1) {
+            // ---- MMA issue: a thread for each stream (its warp finds the segments), so
+            // that a stream waits only for its own
+            const int x = wid - kIssuer;
             const uint32_t idesc_s = f8_idesc(kKeys), idesc_o = f8_idesc(D);
+            const uint32_t sd = tmem + 256 * x, od = sd + 128;
             int base = 0, nseg = 0;  // stages before the segment; segments so far
-            uint32_t sn[2] = {0, 0};  // steps of each stream so far
+            uint32_t sn = 0;         // steps so far
             for (long long u = u0; u < u1; ++nseg) {
                 const Segment s = locate(sq, c.B, G, TR, u, u1);
-                const int stages = (s.pe - s.p0 + 1) / 2;
-                const int steps[2] = {TWO ? stages : (stages + 1) / 2, TWO ? stages : stages / 2};
+                const int stages = (s.pe - s.p0 + 1) / 2, steps = TWO ? stages : (stages + 1 - x) / 2;
                 u += s.p1 - s.p0;
                 __syncwarp();
                 if (lane != 0) continue;
                 wait_or_abort(&ct->q_ready, nseg & 1, p, &ct->abort);
                 tc_fence_after();
-                auto stage_of = [&](int x, int i) { return base + (TWO ? i : 2 * i + x); };
-                auto issue_s = [&](int x, int i) {
-                    const int it = stage_of(x, i), st = it % NS;
+                const uint32_t qa = smem_u32(qbuf) + (TWO ? x * kQ : 0);
+                for (int i = 0; i < steps; ++i, ++sn) {
+                    const int it = base + (TWO ? i : 2 * i + x), st = it % NS;
+                    const uint32_t ka = smem_u32(smem + st * kStage), va = ka + 2 * kPageBytes;
                     wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);
-                    if (*reinterpret_cast<volatile int *>(&ct->abort)) return;
-                    const uint32_t qa = smem_u32(qbuf) + (TWO ? x * kQ : 0), ka = smem_u32(smem + st * kStage);
+                    // the scores take the place of the last step's weights
+                    if (i > 0) wait_or_abort(&ct->o_ready[x], (sn - 1) & 1, p, &ct->abort);
+                    if (*reinterpret_cast<volatile int *>(&ct->abort)) continue;
+                    tc_fence_after();
 #pragma unroll
                     for (int dg = 0; dg < 2; ++dg)
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k) {
                             const uint32_t a = qa + dg * (kRows * D) + 32 * k, b = ka + 32 * k;
-                            mma_f8(tmem + 256 * x, D == 128 ? sw128_desc(a) : sw64_desc(a),
-                                   D == 128 ? sw128_desc(b) : sw64_desc(b), idesc_s, dg + k > 0);
+                            mma_f8(sd, D == 128 ? sw128_desc(a) : sw64_desc(a), D == 128 ? sw128_desc(b) : sw64_desc(b),
+                                   idesc_s, dg + k > 0);
                         }
                     tc_commit(&ct->s_ready[x]);
-                };
-                auto issue_o = [&](int x, int i) {
-                    const int it = stage_of(x, i), st = it % NS;
-                    wait_or_abort(&ct->p_ready[x], (sn[x] + i) & 1, p, &ct->abort);
-                    if (*reinterpret_cast<volatile int *>(&ct->abort)) return;
+                    wait_or_abort(&ct->p_ready[x], sn & 1, p, &ct->abort);
+                    if (*reinterpret_cast<volatile int *>(&ct->abort)) continue;
                     tc_fence_after();
-                    const uint32_t va = smem_u32(smem + st * kStage) + 2 * kPageBytes;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // 32 tokens each: two of each page
 #pragma unroll
                         for (int dg = 0; dg < 2; ++dg)
-                            mma_f8_ts(tmem + 256 * x + 128, tmem + 256 * x + 16 * k + 8 * dg,
-                                      sw64_desc(va + (k >> 1) * kPageBytes + 32 * (k & 1)), idesc_o, i + k + dg > 0);
+                            mma_f8_ts(od, sd + 16 * k + 8 * dg, sw64_desc(va + (k >> 1) * kPageBytes + 32 * (k & 1)), idesc_o,
+                                      i + k + dg > 0);
                     tc_commit(&ct->o_ready[x]);
                     tc_commit(&ct->empty[st]);
-                };
-                for (int x = 0; x < 2; ++x)
-                    if (steps[x] > 0) issue_s(x, 0);
-                for (int i = 0; i < steps[0]; ++i)
-                    for (int x = 0; x < 2; ++x)
-                        if (i < steps[x]) {
-                            issue_o(x, i);
-                            if (i + 1 < steps[x]) {
-                                // the next scores take the place of these weights
-                                wait_or_abort(&ct->o_ready[x], (sn[x] + i) & 1, p, &ct->abort);
-                                issue_s(x, i + 1);
-                            }
-                        }
-                for (int x = 0; x < 2; ++x) sn[x] += steps[x];
+                }
                 base += stages;
             }
             if (lane == 0 && *reinterpret_cast<volatile int *>(&ct->abort)) {
                 // no block ends with products in flight
-                tc_commit(&ct->drained);
+                tc_commit(&ct->drained[x]);
                 const uint64_t t0 = gtimer();
-                while (!mbar_test(&ct->drained, 0) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
+                while (!mbar_test(&ct->drained[x], 0) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
                 }
             }
         }
     } else {
-        // ---- softmax: stream x, a thread a row
+        // ---- softmax: stream x, thread pairs (in two warpgroups) share a row; page y
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
-        const int x = wid >> 2, row = tid & (kRows - 1);
+        const int x = wid >> 3, y = (wid >> 2) & 1, row = tid & (kRows - 1);
         const uint32_t lanes = static_cast<uint32_t>(wid & 3) << 21;  // this warp's tensor-memory lanes
         const uint32_t ts = tmem + 256 * x + lanes, to = ts + 128;
+        auto stream_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(2 + x), "n"(kStream) : "memory"); };
         int base = 0;
         uint32_t sn = 0, on[2] = {0, 0};  // this stream's steps so far; both streams'
         for (long long u = u0; u < u1;) {
@@ -359,103 +340,102 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b];
             const int stages = (s.pe - s.p0 + 1) / 2;
             const int steps = TWO ? stages : (stages + 1 - x) / 2;
-            // queries: 64 rows at a time, two threads a row
+            const int row0 = s.tile * TR + (TWO ? kRows * x : 0);  // of the stream
+            // queries: two neighbouring threads a row
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // both streams are done with the last
-            for (int part = 0; part < (TWO ? 2 : 1); ++part) {
-                const int qr = 64 * (TWO ? part : x) + (row >> 1);  // row of the 128-row tile
-                const int r = s.tile * TR + (TWO ? kRows * x : 0) + qr;
-                const float f = put_query<D>(qbuf + (TWO ? x * kQ : 0), qr, row & 1,
+            if (TWO || x == 0) {
+                const int qr = (tid & (kStream - 1)) >> 1, r = row0 + qr;
+                const float f = put_query<D>(qbuf + (TWO ? x * kQ : 0), qr, tid & 1,
                                              p.q + static_cast<long long>(q0 + r / G) * p.q_stride + (s.h * G + r % G) * D,
                                              r < rows, p.scale_log2);
-                if ((row & 1) == 0) ct->qs[TWO ? x : 0][qr] = f;
+                if ((tid & 1) == 0) ct->qs[TWO ? x : 0][qr] = f;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             mbar_arrive(&ct->q_ready);
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-            const int r = s.tile * TR + (TWO ? kRows * x : 0) + row;
+            const int r = row0 + row;
             const float qs = ct->qs[TWO ? x : 0][row];
             const int sees = r < rows ? row_sees(len, n, G, r) : 0;
-            const int tile_sees = row_sees(len, n, G, s.tile * TR + (TWO ? kRows * x : 0));  // the least of the stream's rows
+            const int tile_sees = row_sees(len, n, G, row0);  // the least of the stream's rows
 
             float ref = -INFINITY, l = 0.f;
             for (int i = 0; i < steps; ++i) {
                 const int it = base + (TWO ? i : 2 * i + x), st = it % NS;
-                wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);  // the pages' scales
+                wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);  // the page's scales
                 wait_or_abort(&ct->s_ready[x], (sn + i) & 1, p, &ct->abort);
                 __syncwarp();
                 tc_fence_after();
-                const float ks[2] = {ct->ks[st][0], ct->ks[st][1]}, vs[2] = {ct->vs[st][0], ct->vs[st][1]};
-                const int tok0 = (s.p0 + 2 * (it - base)) * kPage;
-                const bool edge = tok0 + kKeys > tile_sees || tok0 + kKeys > s.pe * kPage || ks[0] < 0.f || ks[1] < 0.f;
-                // the last token of each page that this row sees, from the page's first
-                int lim[2];
+                // the row's scores of this page
+                float a[64];
+                tc_ld32(ts + 64 * y, *reinterpret_cast<float(*)[32]>(a));
+                tc_ld32(ts + 64 * y + 32, *reinterpret_cast<float(*)[32]>(a + 32));
+                const float ks = ct->ks[st][y], vs = ct->vs[st][y];
+                const int pg = s.p0 + 2 * (it - base) + y;
+                const bool none = ks < 0.f || pg >= s.pe;  // no such page
+                const float fs = qs * ks;
+                tc_wait_ld();
+                if (none || (pg + 1) * kPage > tile_sees) {
+                    const int lim = none ? 0 : sees - pg * kPage;
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    lim[y] = ks[y] < 0.f || tok0 + y * kPage >= s.pe * kPage ? 0 : sees - (tok0 + y * kPage);
-                // largest of the row
-                float mx = -INFINITY;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float a[32];
-                    tc_ld32(ts + 32 * h, a);
-                    tc_wait_ld();
-                    const float fs = qs * ks[h >> 1];
-                    float mh = -INFINITY;
-                    if (edge) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (32 * (h & 1) + j < lim[h >> 1]) mh = fmaxf(mh, a[j] * fs);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) mh = fmaxf(mh, a[j] * fs);
-                    }
-                    mx = fmaxf(mx, mh + scale_log2(vs[h >> 1]));
+                    for (int j = 0; j < 64; ++j)
+                        if (j >= lim) a[j] = -INFINITY;
                 }
+                // their largest, in log2 units (a row's factor is not negative), with the other page's
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 64; j += 8)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) m4[z] = fmaxf(m4[z], fmaxf(a[j + z], a[j + 4 + z]));
+                const float mr = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                float mx = mr > -INFINITY ? mr * fs + scale_log2(vs) : -INFINITY;
+                ct->mx[x][y][row] = mx;
+                tc_fence_before();
+                stream_sync();  // (the weights overwrite the other page's scores: they have been read)
+                tc_fence_after();
+                mx = fmaxf(mx, ct->mx[x][y ^ 1][row]);
                 const bool move = mx > ref + kSlack;  // (ref = -inf: as soon as anything is seen)
                 if (__any_sync(0xffffffffu, move)) {
                     const float nref = move ? mx : ref;
                     const float f = move ? ex2(ref - nref) : 1.f;
                     l *= f;
                     ref = nref;
-                    if (i > 0) {
+                    if (i > 0) {  // this thread's half of the row's accumulators
                         wait_or_abort(&ct->o_ready[x], (sn + i - 1) & 1, p, &ct->abort);
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
                         for (int h = 0; h < D / 32; ++h) {
-                            float a[32];
-                            tc_ld32(to + 32 * h, a);
+                            float v[16];
+                            uint32_t b[16];
+                            tc_ld16(to + (D / 2) * y + 16 * h, v);
                             tc_wait_ld();
-                            uint32_t b[2][16];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) b[j >> 4][j & 15] = __float_as_uint(a[j] * f);
-                            tc_st16(to + 32 * h, b[0]);
-                            tc_st16(to + 32 * h + 16, b[1]);
+                            for (int j = 0; j < 16; ++j) b[j] = __float_as_uint(v[j] * f);
+                            tc_st16(to + (D / 2) * y + 16 * h, b);
                         }
-                        tc_wait_st();
                     }
                 }
-                const float base_ref = ref == -INFINITY ? 0.f : ref;
-                // weights and their digits, 32 tokens at a time, over the scores read
+                // 64 w vs as digits, 32 tokens at a time; w's sum from theirs
+                const float pv = fmaxf(vs, 0x1p-64f) * kGain;
+                const float add = __log2f(pv) - (ref == -INFINITY ? 0.f : ref);
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float a[32];
-                    tc_ld32(ts + 32 * h, a);
-                    tc_wait_ld();
-                    const float fs = qs * ks[h >> 1], pv = vs[h >> 1] * kGain;
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float w = ex2(fmaf(a[j], fs, -base_ref));
-                        if (edge && 32 * (h & 1) + j >= lim[h >> 1]) w = 0.f;
-                        l += w;
-                        a[j] = w * pv;
+                    for (int j = 32 * h; j < 32 * h + 32; ++j) {
+                        a[j] = ex2(fmaf(a[j], fs, add));
+                        l4[j & 3] += a[j];
                     }
                     uint32_t dg[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) digits4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3], dg[j], dg[8 + j]);
-                    tc_st16(ts + 16 * h, dg);
+                    for (int j = 0; j < 8; ++j) {
+                        const float *w = a + 32 * h + 4 * j;
+                        digits4(w[0], w[1], w[2], w[3], dg[j], dg[8 + j]);
+                    }
+                    tc_st16(ts + 32 * y + 16 * h, dg);
                 }
+                l += ((l4[0] + l4[1]) + (l4[2] + l4[3])) * (1.f / pv);
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&ct->p_ready[x]);
@@ -464,71 +444,63 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             on[0] += TWO ? stages : (stages + 1) / 2;
             on[1] += TWO ? stages : stages / 2;
 
-            // ---- the result: o / 64 in tensor memory, the reference and the sum
-            float *part = part_slot(p, blockIdx.x, s.p0 == 0);
-            const int rr = TWO ? kRows * x + row : row;
-            uint16_t *orow = out_row(p, q0, s.h, G, min(r, rows - 1));
-            float f0 = 1.f, f1 = 0.f, lsum = l, msum = ref;
-            if (!TWO) {  // both streams' sums
-                ct->m[x][row] = ref;
-                ct->l[x][row] = l;
-                asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-                const float m0 = ct->m[0][row], m1 = ct->m[1][row], mm = fmaxf(m0, m1);
-                const float mref = mm == -INFINITY ? 0.f : mm;
-                f0 = ex2(m0 - mref);
-                f1 = ex2(m1 - mref);
-                lsum = ct->l[0][row] * f0 + ct->l[1][row] * f1;
-                msum = mm;
-            }
-            const bool have0 = TWO ? steps > 0 : stages > 0, have1 = !TWO && stages > 1;
+            // ---- the result: o / 64 in tensor memory, references and sums
+            if (y == 0) ct->m[x][row] = ref;
+            ct->l[x][y][row] = l;
+            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+            const bool have0 = stages > 0, have1 = !TWO && stages > 1;
             const int x0 = TWO ? x : 0;
             if (have0) wait_or_abort(&ct->o_ready[x0], (on[x0] - 1) & 1, p, &ct->abort);
             if (have1) wait_or_abort(&ct->o_ready[1], (on[1] - 1) & 1, p, &ct->abort);
             __syncwarp();
             tc_fence_after();
-            const float inv = inv_sum(kGain, lsum);
-            if (!s.whole() && (TWO || x == 0)) {
+            float f0 = 1.f, f1 = 0.f, msum = ref, lsum = ct->l[x0][0][row] + ct->l[x0][1][row];
+            if (!TWO) {  // the streams' together
+                const float m0 = ct->m[0][row], m1 = ct->m[1][row];
+                msum = fmaxf(m0, m1);
+                const float mref = msum == -INFINITY ? 0.f : msum;
+                f0 = ex2(m0 - mref);
+                f1 = ex2(m1 - mref);
+                lsum = lsum * f0 + (ct->l[1][0][row] + ct->l[1][1][row]) * f1;
+            }
+            float *part = part_slot(p, blockIdx.x, s.p0 == 0);
+            const int rr = TWO ? kRows * x + row : row;
+            if (!s.whole() && y == 0 && (TWO || x == 0)) {
                 part[rr] = msum;
                 part[TR + rr] = lsum;
             }
-            constexpr int NH = TWO ? D / 32 : D / 64;  // 32-column pieces of this thread: all, or the stream's half
+            const float inv = inv_sum(kGain, lsum);
+            uint16_t *orow = out_row(p, q0, s.h, G, min(r, rows - 1));
+            constexpr int kCols = TWO ? D / 2 : D / 4;  // of this thread
+            const int col0 = kCols * (TWO ? y : 2 * x + y);
 #pragma unroll 1
-            for (int h = 0; h < NH; ++h) {
-                const int col = 32 * (TWO ? h : NH * x + h);
-                float a[32];
+            for (int col = col0; col < col0 + kCols; col += 16) {
+                float v[16], w[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) a[j] = 0.f;
-                if (have0) {
-                    tc_ld32(tmem + lanes + 256 * x0 + 128 + col, a);
-                    tc_wait_ld();
-                }
+                for (int j = 0; j < 16; ++j) v[j] = w[j] = 0.f;
+                if (have0) tc_ld16(tmem + lanes + 256 * x0 + 128 + col, v);
+                if (have1) tc_ld16(tmem + lanes + 256 + 128 + col, w);
+                tc_wait_ld();
                 if (!TWO) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) a[j] *= f0;
-                    if (have1) {
-                        float b[32];
-                        tc_ld32(tmem + lanes + 256 + 128 + col, b);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) a[j] += b[j] * f1;
-                    }
+                    for (int j = 0; j < 16; ++j) v[j] = v[j] * f0 + w[j] * f1;
                 }
                 if (!s.whole()) {
                     float4 *o = reinterpret_cast<float4 *>(part + 2 * TR + rr * D + col);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                    for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else if (r < rows) {
                     uint4 *o = reinterpret_cast<uint4 *>(orow + col);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = make_uint4(pack_bf16(a[8 * j] * inv, a[8 * j + 1] * inv),
-                                          pack_bf16(a[8 * j + 2] * inv, a[8 * j + 3] * inv),
-                                          pack_bf16(a[8 * j + 4] * inv, a[8 * j + 5] * inv),
-                                          pack_bf16(a[8 * j + 6] * inv, a[8 * j + 7] * inv));
+                    for (int j = 0; j < 2; ++j)
+                        o[j] = make_uint4(pack_bf16(v[8 * j] * inv, v[8 * j + 1] * inv),
+                                          pack_bf16(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
+                                          pack_bf16(v[8 * j + 4] * inv, v[8 * j + 5] * inv),
+                                          pack_bf16(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
                 }
             }
             tc_fence_before();
-            if (!s.whole()) join_tile<D>(p, s, U, blocks, TR, rows, q0, G, kGain, &ct->last);
+            if (!s.whole()) join_tile<D, kConsumers>(p, s, U, blocks, TR, rows, q0, G, kGain, &ct->last);
             base += stages;
             u += s.p1 - s.p0;
         }
@@ -537,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (wid == 9) tc_dealloc(tmem, kTmemCols);
+    if (wid == kIssuer) tc_dealloc(tmem, kTmemCols);
 }
 
 template <int D, bool TWO>
