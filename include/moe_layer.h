@@ -62,7 +62,7 @@ moe_status_t moe_norm(const void *x_dev, int x_f32, int64_t x_stride, const void
  *   q_dev uint8 [N, K/2], s_dev uint8 [N, K/16], ts_dev float [N]
  *   x_dev bf16 [T, K], rows x_stride elements apart
  *   y_dev float [T, N] (y_bf16 = 0) or bf16 (1), contiguous, fully written
- *   N >= 1, K a positive multiple of 32, T >= 0 (0: a no-op).  Meant for decode
+ *   N >= 1, K a multiple of 32 up to 2^22, T >= 0 (0: a no-op).  Meant for decode
  *   batches: up to 24 tokens read the weights once; more run in groups of 24,
  *   each reading them again (from L2 as far as they fit).
  * q_dev and x_dev 16-byte aligned, s_dev 2-byte, ts_dev 4-byte, y_dev to its

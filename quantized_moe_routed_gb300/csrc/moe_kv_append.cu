@@ -27,70 +27,118 @@ namespace {
 #include "moe_layer_device.cuh"
 
 constexpr int kPage = MOE_KV_PAGE;
-constexpr int kThreads = 256;
 // 448 * 2^60, what the largest scale holds: attention's softmax weights are
 // taken relative to the largest (weight x v scale), and this range of scales
 // keeps the smallest ones that count inside fp32.
 constexpr float kMaxValue = 448.f * 1152921504606846976.f;
 
-// The elements of rotated pair j (j < rot / 2); pairs past it are (2j, 2j + 1).
-__device__ __forceinline__ void pair_at(const KvParams &c, int j, int &i0, int &i1)
-{
-    const bool half = j < c.rot_dim / 2 && !c.rot_inter;
-    i0 = half ? j : 2 * j;
-    i1 = half ? j + c.rot_dim / 2 : 2 * j + 1;
-}
+// Which elements a rotation pairs: neighbours; element i of the two halves, where
+// 16 divides rot_dim; the same otherwise.
+enum Rot { kNone, kNeighbours, kHalves, kOddHalves };
 
-// Rotate pair (a, b) by the table's angle; every product and sum rounded on
-// its own, so that the codes are those of the formula in fp32.
-__device__ __forceinline__ void rotate(float &a, float &b, float2 cs)
-{
-    const float ra = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-    const float rb = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
-    a = ra;
-    b = rb;
-}
+// A unit is 16 elements of a head that a thread holds: 8 from c0 on and 8 from c1
+// on, which are each other's partners in the rotated part of kHalves, else lie
+// one after the other.
+template <Rot ROT>
+struct Units {
+    int c0, c1;
+    __device__ __forceinline__ Units(const KvParams &c, int u)
+    {
+        const bool apart = ROT == kHalves && u < c.rot_dim / 16;
+        c0 = apart ? 8 * u : 16 * u;
+        c1 = apart ? c0 + c.rot_dim / 2 : 16 * u + 8;
+    }
+};
 
-// cnt tokens of D bf16 (src, stride elements apart) as fp32 into t[cnt][D + 1].
-template <int D>
-__device__ __forceinline__ void load_tile(float *t, const uint16_t *src, long long stride, int cnt)
+__device__ __forceinline__ void load8(float *v, const uint16_t *src)
 {
-    for (int i = threadIdx.x; i < cnt * (D / 8); i += kThreads) {
-        const int tok = i / (D / 8), c = (i % (D / 8)) * 8;
-        const uint4 a = *reinterpret_cast<const uint4 *>(src + tok * stride + c);
-        float *o = t + tok * (D + 1) + c;
+    const uint4 a = *reinterpret_cast<const uint4 *>(src);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            o[2 * j] = bf16_lo(u4w(a, j));
-            o[2 * j + 1] = bf16_hi(u4w(a, j));
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(u4w(a, j));
+        v[2 * j + 1] = bf16_hi(u4w(a, j));
+    }
+}
+
+// The (cos, sin) of the unit's eight pairs (pairs of the table 8 u .. 8 u + 7; (1,
+// 0) past the rotated part).
+template <Rot ROT>
+__device__ __forceinline__ void load_angles(const KvParams &c, float2 (&cs)[8], int pos, int u)
+{
+    if (ROT == kNone || ROT == kOddHalves) return;
+    const float2 *t = reinterpret_cast<const float2 *>(c.rope + static_cast<size_t>(pos) * c.rot_dim) + 8 * u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = 8 * u + i < c.rot_dim / 2 ? __ldg(t + i) : make_float2(1.f, 0.f);
+}
+
+// (a, b) turned: every product and sum rounded on its own, so that the values are
+// those of the formula in fp32.
+__device__ __forceinline__ float turn_a(float a, float b, float2 cs)
+{
+    return __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+}
+__device__ __forceinline__ float turn_b(float a, float b, float2 cs)
+{
+    return __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+}
+
+// A head's unit, rotated.
+template <Rot ROT>
+__device__ __forceinline__ void load_unit(const KvParams &c, float (&v)[16], const uint16_t *head, const Units<ROT> &un,
+                                          const float2 (&cs)[8], int pos)
+{
+    load8(v, head + un.c0);
+    load8(v + 8, head + un.c1);
+    if (ROT == kNeighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (un.c0 + 2 * i < c.rot_dim) {
+                const float a = v[2 * i], b = v[2 * i + 1];
+                v[2 * i] = turn_a(a, b, cs[i]);
+                v[2 * i + 1] = turn_b(a, b, cs[i]);
+            }
+    } else if (ROT == kHalves) {
+        if (un.c0 < c.rot_dim / 2) {  // (a rotated unit begins in the first half)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = v[i], b = v[8 + i];
+                v[i] = turn_a(a, b, cs[i]);
+                v[8 + i] = turn_b(a, b, cs[i]);
+            }
+        }
+    } else if (ROT == kOddHalves) {
+        const int half = c.rot_dim / 2;
+        const float2 *t = reinterpret_cast<const float2 *>(c.rope + static_cast<size_t>(pos) * c.rot_dim);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int d = un.c0 + i;
+            if (d >= c.rot_dim) continue;
+            const float o = __uint_as_float(static_cast<uint32_t>(head[d < half ? d + half : d - half]) << 16);
+            v[i] = d < half ? turn_a(v[i], o, __ldg(t + d)) : turn_b(o, v[i], __ldg(t + d - half));
         }
     }
 }
 
-// Rotate the tile in place: token i is at position pos0 + i.
-template <int D>
-__device__ __forceinline__ void rotate_tile(const KvParams &c, float *t, int cnt, int pos0)
-{
-    const int np = c.rot_dim / 2;
-    for (int i = threadIdx.x; i < cnt * np; i += kThreads) {
-        const int tok = i / np, j = i % np;
-        int i0, i1;
-        pair_at(c, j, i0, i1);
-        const float2 cs = __ldg(reinterpret_cast<const float2 *>(c.rope + static_cast<size_t>(pos0 + tok) * c.rot_dim) + j);
-        rotate(t[tok * (D + 1) + i0], t[tok * (D + 1) + i1], cs);
-    }
-}
-
-__device__ __forceinline__ float block_max(float v, float *red)
+// The block's largest of a and of b.
+template <int THREADS>
+__device__ __forceinline__ void block_max2(float &a, float &b, float *red)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    for (int o = 16; o > 0; o >>= 1) {
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+    }
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+        red[2 * w] = a;
+        red[2 * w + 1] = b;
+    }
     __syncthreads();
-    v = red[0];
-    for (int i = 1; i < kThreads / 32; ++i) v = fmaxf(v, red[i]);
-    __syncthreads();
-    return v;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        a = fmaxf(a, red[2 * i]);
+        b = fmaxf(b, red[2 * i + 1]);
+    }
 }
 
 // Sixteen codes times f (a power of two, or a ratio of caller's scales).
@@ -120,11 +168,14 @@ __device__ __forceinline__ float new_scale(float amax, bool old_tokens, float ol
     return s;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) moe_kv_append_kernel(const AppendParams p)
+template <int D, Rot ROT>
+__global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) moe_kv_append_kernel(const AppendParams p)
 {
-    extern __shared__ float tile[];  // [2][kPage][D + 1]: k, v (or one query head)
-    __shared__ float red[kThreads / 32];
+    constexpr int UT = D / 16;            // units of a token
+    constexpr int kThreads = kPage * UT;  // a unit of a full page each
+    constexpr int kStride = kPage + 4;          // bytes of a v row in shared memory: no bank twice
+    __shared__ uint32_t vt[D * kStride / 4];    // v codes, transposed
+    __shared__ float red[2 * kThreads / 32];
     __shared__ int bad_tok[kPage];
     const KvParams &c = p.c;
     grid_wait();
@@ -160,100 +211,111 @@ __global__ void __launch_bounds__(kThreads) moe_kv_append_kernel(const AppendPar
         if (!ok && tid == 0) atomicOr(c.ctrl + 2, kErrBadIndex);
         if (queries) {
             const int G = c.q_heads / hk;
-            for (int g = 0; g < G; ++g) {
-                const int hq = h * G + g;
-                __syncthreads();
-                load_tile<D>(tile, p.q + row0 * p.q_stride + hq * D, p.q_stride, cnt);
-                __syncthreads();
-                if (ok) rotate_tile<D>(c, tile, cnt, pos0);
-                __syncthreads();
-                for (int i = tid; i < cnt * (D / 8); i += kThreads) {
-                    const int tok = i / (D / 8), cc = (i % (D / 8)) * 8;
-                    const float *t = tile + tok * (D + 1) + cc;
-                    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                    if (ok)
-                        o = make_uint4(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]), pack_bf16(t[4], t[5]),
-                                       pack_bf16(t[6], t[7]));
-                    *reinterpret_cast<uint4 *>(p.q_out + (static_cast<size_t>(row0 + tok) * c.q_heads + hq) * D + cc) = o;
+            if (const int tok = tid / UT, u = tid % UT; tok < cnt) {
+                const Units<ROT> un(c, u);
+                float2 cs[8];
+                if (ok) load_angles<ROT>(c, cs, pos0 + tok, u);
+                const uint16_t *src = p.q + (row0 + tok) * p.q_stride + h * G * D;
+                uint16_t *dst = p.q_out + (static_cast<size_t>(row0 + tok) * c.q_heads + h * G) * D;
+#pragma unroll 2
+                for (int g = 0; g < G; ++g) {
+                    float v[16];
+                    if (ok) {
+                        load_unit<ROT>(c, v, src + g * D, un, cs, pos0 + tok);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        *reinterpret_cast<uint4 *>(dst + g * D + (y ? un.c1 : un.c0)) =
+                            make_uint4(pack_bf16(v[8 * y], v[8 * y + 1]), pack_bf16(v[8 * y + 2], v[8 * y + 3]),
+                                       pack_bf16(v[8 * y + 4], v[8 * y + 5]), pack_bf16(v[8 * y + 6], v[8 * y + 7]));
                 }
             }
             continue;
         }
         if (!ok) continue;
-        float *tk = tile, *tv = tile + kPage * (D + 1);
         const size_t ph = static_cast<size_t>(id) * hk + h;
         const float old_ks = c.ks[ph], old_vs = c.vs[ph];
-        __syncthreads();
+        __syncthreads();  // the last page's readers of shared memory are done
         if (tid < kPage) bad_tok[tid] = 0;
-        load_tile<D>(tk, p.k + row0 * p.k_stride + h * D, p.k_stride, cnt);
-        load_tile<D>(tv, p.v + row0 * p.v_stride + h * D, p.v_stride, cnt);
         __syncthreads();
-        rotate_tile<D>(c, tk, cnt, pos0);
-        __syncthreads();
-        for (int i = tid; i < cnt * D; i += kThreads) {
-            const int o = (i / D) * (D + 1) + i % D;
-            if (!(fabsf(tk[o]) <= kMaxValue) || !(fabsf(tv[o]) <= kMaxValue)) bad_tok[i / D] = 1;
+        const int tok = tid / UT, u = tid % UT;
+        const bool in = tok < cnt;
+        const Units<ROT> un(c, u);
+        float x[16], z[16];  // the thread's unit of k and of v
+        if (in) {
+            float2 cs[8];
+            load_angles<ROT>(c, cs, pos0 + tok, u);
+            load_unit<ROT>(c, x, p.k + (row0 + tok) * p.k_stride + h * D, un, cs, pos0 + tok);
+            load_unit<kNone>(c, z, p.v + (row0 + tok) * p.v_stride + h * D, Units<kNone>(c, u), cs, pos0 + tok);
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) bad |= !(fabsf(x[j]) <= kMaxValue) || !(fabsf(z[j]) <= kMaxValue);
+            if (bad) bad_tok[tok] = 1;
         }
         __syncthreads();
         float ak = 0.f, av = 0.f;
-        for (int i = tid; i < cnt * D; i += kThreads) {
-            const int o = (i / D) * (D + 1) + i % D;
-            if (bad_tok[i / D]) {
-                tk[o] = __int_as_float(0x7FC00000);
-                tv[o] = 0.f;
-            } else {
-                ak = fmaxf(ak, fabsf(tk[o]));
-                av = fmaxf(av, fabsf(tv[o]));
+        if (in) {
+            const bool bad = bad_tok[tok] != 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (bad) {
+                    x[j] = __int_as_float(0x7FC00000);
+                    z[j] = 0.f;
+                } else {
+                    ak = fmaxf(ak, fabsf(x[j]));
+                    av = fmaxf(av, fabsf(z[j]));
+                }
             }
         }
-        ak = block_max(ak, red);
-        av = block_max(av, red);
+        block_max2<kThreads>(ak, av, red);
         float fk, fv;
         const float sk = new_scale(ak, slot0 > 0, old_ks, fk), sv = new_scale(av, slot0 > 0, old_vs, fv);
         const float ik = 1.f / sk, iv = 1.f / sv;
-        // k: a token's codes are contiguous
+        // k: a token's codes are contiguous; v goes through shared memory, transposed
         uint8_t *ko = c.k + ph * (kPage * D);
-        for (int i = tid; i < kPage * (D / 16); i += kThreads) {
-            const int tok = i / (D / 16), cc = (i % (D / 16)) * 16, r = tok - slot0;
-            uint4 *dst = reinterpret_cast<uint4 *>(ko + tok * D + cc);
-            if (r >= 0 && r < cnt) {
-                const float *t = tk + r * (D + 1) + cc;
-                uint32_t o[4];
+        if (in) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[j] = e4m3_pack4(t[4 * j] * ik, t[4 * j + 1] * ik, t[4 * j + 2] * ik, t[4 * j + 3] * ik);
-                *dst = make_uint4(o[0], o[1], o[2], o[3]);
-            } else if (fk != 1.f) {
-                *dst = requant16(*dst, fk);
+            for (int y = 0; y < 2; ++y) {
+                uint2 o;
+                o.x = e4m3_pack4(x[8 * y] * ik, x[8 * y + 1] * ik, x[8 * y + 2] * ik, x[8 * y + 3] * ik);
+                o.y = e4m3_pack4(x[8 * y + 4] * ik, x[8 * y + 5] * ik, x[8 * y + 6] * ik, x[8 * y + 7] * ik);
+                *reinterpret_cast<uint2 *>(ko + (slot0 + tok) * D + (y ? un.c1 : un.c0)) = o;
+            }
+            uint8_t *t = reinterpret_cast<uint8_t *>(vt) + 16 * u * kStride + slot0 + tok;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                const uint32_t w = e4m3_pack4(z[j] * iv, z[j + 1] * iv, z[j + 2] * iv, z[j + 3] * iv);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) t[(j + b) * kStride] = static_cast<uint8_t>(w >> (8 * b));
             }
         }
+        if (fk != 1.f && (tok < slot0 || tok >= slot0 + cnt)) {  // the page's other codes: a granule a thread
+            uint4 *dst = reinterpret_cast<uint4 *>(ko + tid * 16);
+            *dst = requant16(*dst, fk);
+        }
+        __syncthreads();
         // v: a head dimension's codes are contiguous; sixteen tokens at a time
         uint8_t *vo = c.v + ph * (kPage * D);
         for (int i = tid; i < D * (kPage / 16); i += kThreads) {
             const int d = i % D, s0 = (i / D) * 16;
-            const int lo = max(slot0 - s0, 0), hi = min(slot0 + cnt - s0, 16);
+            const int lo = max(slot0 - s0, 0), hi = min(slot0 + cnt - s0, 16);  // the new ones
             uint4 *dst = reinterpret_cast<uint4 *>(vo + d * kPage + s0);
-            const bool some = lo < hi;
-            if (!some && fv == 1.f) continue;
+            if (lo >= hi && fv == 1.f) continue;
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (!(lo == 0 && hi == 16)) {
+            if (lo > 0 || hi < 16) {
                 w = *dst;
                 if (fv != 1.f) w = requant16(w, fv);
             }
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t m = 0u, x[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int tok = 4 * j + u;
-                    const bool in = tok >= lo && tok < hi;
-                    x[u] = __float_as_uint(in ? tv[(s0 + tok - slot0) * (D + 1) + d] * iv : 0.f);
-                    if (in) m |= 0xFFu << (8 * u);
-                }
-                o[j] = (e4m3_pack4(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
-                                   __uint_as_float(x[3])) & m) |
-                       (u4w(w, j) & ~m);
+                // bytes lo - 4 j .. hi - 4 j - 1 of the word are new
+                const int a = min(max(lo - 4 * j, 0), 4), b = min(max(hi - 4 * j, 0), 4);
+                const uint32_t m = b <= a ? 0u : (0xFFFFFFFFu >> (32 - 8 * (b - a))) << (8 * a);
+                o[j] = (vt[(d * kStride + s0) / 4 + j] & m) | (u4w(w, j) & ~m);
             }
             *dst = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -264,18 +326,23 @@ __global__ void __launch_bounds__(kThreads) moe_kv_append_kernel(const AppendPar
     }
 }
 
-template <int D>
-cudaError_t launch_d(const AppendParams &p, cudaStream_t st)
+template <int D, Rot ROT>
+cudaError_t launch_one(const AppendParams &p, cudaStream_t st)
 {
-    const int smem = 2 * kPage * (D + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(moe_kv_append_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     const KvParams &c = p.c;
     // pages a sequence's new tokens can touch; a block walks on where max_q was
     // given too small
     const int pages = std::min(std::max(c.max_q, 1) / kPage + 2, c.max_pages);
-    LaunchCfg l(dim3(c.max_q <= 1 ? 1 : pages, c.B, c.kv_heads * (p.q ? 2 : 1)), dim3(kThreads), smem, st);
-    return cudaLaunchKernelEx(&l.cfg, moe_kv_append_kernel<D>, p);
+    LaunchCfg l(dim3(c.max_q <= 1 ? 1 : pages, c.B, c.kv_heads * (p.q ? 2 : 1)), dim3(kPage * D / 16), 0, st);
+    return cudaLaunchKernelEx(&l.cfg, moe_kv_append_kernel<D, ROT>, p);
+}
+
+template <int D>
+cudaError_t launch_d(const AppendParams &p, cudaStream_t st)
+{
+    if (p.c.rot_dim == 0) return launch_one<D, kNone>(p, st);
+    if (p.c.rot_inter) return launch_one<D, kNeighbours>(p, st);
+    return p.c.rot_dim % 16 == 0 ? launch_one<D, kHalves>(p, st) : launch_one<D, kOddHalves>(p, st);
 }
 
 }  // namespace

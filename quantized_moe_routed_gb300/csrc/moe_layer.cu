@@ -25,6 +25,7 @@ struct moe_kv {
 namespace {
 
 constexpr int kMaxNormH = 16384;
+constexpr int kMaxLinearK = 1 << 22;  // the kernel counts bytes inside 512 rows in 32 bits
 // the kernels count tokens and units of a sequence in 32 bits
 constexpr int kMaxSeqPages = 1 << 24;
 constexpr int kMaxStepRows = 1 << 30;  // new tokens x query heads of a step
@@ -160,8 +161,8 @@ moe_status_t moe_linear(const uint8_t *q_dev, const uint8_t *s_dev, const float 
                         const void *x_dev, int64_t x_stride, void *y_dev, int y_bf16, int T, void *stream)
 {
     if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T=%d is negative", T);
-    if (N < 1 || K < 32 || K % 32)
-        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "N=%d must be positive and K=%d a positive multiple of 32", N, K);
+    if (N < 1 || K < 32 || K % 32 || K > kMaxLinearK)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "N=%d must be positive and K=%d a multiple of 32 up to %d", N, K, kMaxLinearK);
     if (T > 65535 * moe::kLinearMaxT) return fail(MOE_ERR_INVALID_ARG, "T=%d is more than a launch takes", T);
     if (y_bf16 != 0 && y_bf16 != 1) return fail(MOE_ERR_INVALID_ARG, "y_bf16=%d is not 0 or 1", y_bf16);
     if (x_stride < K) return fail(MOE_ERR_INVALID_ARG, "x_stride=%lld < K=%d", static_cast<long long>(x_stride), K);
