@@ -4,29 +4,31 @@
 //   o[i, h] = sum_t w_t v[t] / sum_t w_t,   w_t = 2^(s_t - ref),
 //   s_t = log2(e) scale q.k_t
 //
-// Both products run on the tensor cores (tcgen05.mma kind::f8f6f4, accumulators
-// in tensor memory) straight on the cache's E4M3 codes, which TMA brings into
-// shared memory and nothing else touches:
+// Both products run on the tensor cores (tcgen05.mma), their accumulators in
+// tensor memory:
 //
-//  * S[128 rows x 128 tokens] = Q K^T: q enters as two E4M3 digits, hi + lo,
-//    after a power-of-two prescale of the row (largest magnitude into [128,
-//    256)): 8 significant bits are two digits of 4, so the sum is exact down
-//    to 2^-10 of the row's largest.
-//  * O[128 rows x head dim] += P V: the weights 64 w vs (vs: the page's v scale
-//    over the largest that the reference allows for) enter as two digits, relative
-//    error 2^-9, written to tensor memory over the scores they come from.
+//  * S[128 rows x 128 tokens] = Q K^T, kind::f8f6f4 on the cache's E4M3 codes as TMA
+//    brings them: q enters as two E4M3 digits, hi + lo, after a power-of-two
+//    prescale of the row (largest magnitude into [128, 256)): 8 significant bits
+//    are two digits of 4, so the sum is exact down to 2^-10 of the row's
+//    largest.  Two digits at twice the 16-bit rate cost what 16-bit operands would.
+//  * O[128 rows x head dim] += P V, kind::f16: the weights 64 w vs (vs: the page's v
+//    scale over the largest that the reference allows for) are rounded to fp16 and
+//    written to tensor memory over the scores they come from.  v's codes become
+//    fp16 (exact) in shared memory, once for all rows of the block; digits for the
+//    weights instead would cost the softmax threads, which bound the kernel, three
+//    more instructions a weight.
 //
-// Two digits at twice the 16-bit rate cost what 16-bit operands would, without
-// converting the cache.  The reference is the running maximum of s + ceil(
-// log2(vs)), moved only when a tile exceeds it by more than 2 (the digits hold
-// four times the usual largest), so the accumulators in tensor memory are rescaled rarely.
+// The reference is the running maximum of s + ceil(log2(vs)), moved only when a
+// step exceeds it by more than 8 (fp16 holds 64 * 2^8), so the accumulators in
+// tensor memory are rescaled rarely.
 //
-// A block runs two streams, each with two warpgroups for the softmax (two
-// threads a row, each a page of the stage) and its own S / P and O in tensor memory, so that
-// one stream's softmax and the other's products overlap.  With TWO, the streams are two row tiles
-// that share the pages; otherwise they are the even and the odd page pairs of
-// one row tile, joined at the end.  One warp brings pages (two a stage), one thread a
-// stream issues the MMAs.
+// A block runs two streams, each with a warpgroup for the softmax (a thread a
+// row), a thread that issues its MMAs, and its own S / P and O in tensor memory,
+// so that one stream's softmax and the other's products overlap.  With TWO, the
+// streams are two row tiles that share the pages; otherwise they are the even
+// and the odd page pairs of one row tile, joined at the end.  One warp brings
+// pages, two a stage; a warpgroup converts v.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -44,30 +46,33 @@ namespace {
 
 #include "moe_attend.cuh"
 
-constexpr int kStream = 256;     // softmax threads of a stream
-constexpr int kConsumers = 2 * kStream;
-constexpr int kThreads = kConsumers + 128;  // and a warpgroup with the producer and the MMA issuers
-// Registers a thread of the two kinds keeps: 512 * 104 + 128 * 48 = 59392, within
-// what the block is launched with (640 threads of 96).
-constexpr int kConsumerRegs = 104, kProducerRegs = 48;
-constexpr int kRows = 128;       // rows of a stream: tensor-memory lanes
+constexpr int kRows = 128;       // rows of a stream: tensor-memory lanes, softmax threads
+constexpr int kConsumers = 2 * kRows;
+constexpr int kThreads = kConsumers + 256;  // and a warpgroup that converts v, one with the producer and the issuers
+// Registers a thread of the two kinds keeps: 256 * 200 + 256 * 56 = 65536, what the
+// block is launched with (512 threads of 128).
+constexpr int kConsumerRegs = 200, kOtherRegs = 56;
 constexpr int kKeys = 2 * kPage; // tokens of a stage
-constexpr float kGain = 64.f;    // of the weights' digits
-constexpr float kSlack = 2.f;    // how far a tile may exceed the reference (64 * 2^2 = 256 <= 448)
+constexpr float kGain = 64.f;    // of the weights
+constexpr float kSlack = 8.f;    // how far a step may exceed the reference (64 * 2^8 is inside fp16)
 constexpr int kTmemCols = 512;   // stream s: S / P at 256 s, O at 256 s + 128
+constexpr int kKStages = 3, kVStages = 2;
+constexpr int kScales = 8;       // stages whose scales are kept: more than any warp lags behind the producer
 
 struct Control {
-    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t k_full[kKStages], k_empty[kKStages];   // codes of k
+    uint64_t v_full[kVStages], v_empty[kVStages];   // codes of v
+    uint64_t f_full[2], f_empty[2];                 // v in fp16
+    uint64_t sc_full[kScales];
     uint64_t q_ready, s_ready[2], p_ready[2], o_ready[2], drained[2];
-    float ks[kMaxStages][2], vs[kMaxStages][2];  // scales of the stage's pages; ks < 0: no such page
-    float qs[2][kRows];                          // each row's factor from digits to scores (log2 units)
-    float mx[2][2][kRows];                       // [stream][page]: largest of a row in a stage's page
-    float m[2][kRows], l[2][2][kRows];           // references, and sums of the two pages, at a tile's end
+    float ks[kScales][2], vs[kScales][2];  // scales of a stage's pages; ks < 0: no such page
+    float qs[2][kRows];                    // each row's factor from digits to scores (log2 units)
+    float m[2][kRows], l[2][kRows];        // the streams' references and sums, for joining them
     uint32_t tmem;
     int abort, last;
 };
 
-// D[128 x N] (+)= A B^T with E4M3 operands: A from shared or tensor memory
+// D[128 x N] (+)= A B^T: E4M3 operands, both in shared memory
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
@@ -75,16 +80,17 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// The same for fp16 operands, A in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Instruction descriptor, kind::f8f6f4: fp32 accumulator, E4M3 A and B, K-major
-// both, M = 128, N = n.
-__device__ __forceinline__ uint32_t f8_idesc(int n)
+// Instruction descriptor: fp32 accumulator, E4M3 (kind::f8f6f4) or fp16 (kind::f16)
+// A and B, K-major both, M = 128, N = n.
+__device__ __forceinline__ uint32_t mma_idesc(int n)
 {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
@@ -173,32 +179,71 @@ __device__ __forceinline__ float put_query(uint8_t *dst, int row, int half, cons
     return am >= 0x7F80u ? __int_as_float(0x7FC00000) : exp2i(-e) * fabsf(scale);
 }
 
-template <int D, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __grid_constant__ AttendParams p, int NS)
+// Two packed fp32 values.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
 {
-    constexpr int TR = TWO ? 2 * kRows : kRows;   // query rows of a tile
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+template <int D, bool TWO>
+__global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __grid_constant__ AttendParams p)
+{
+    constexpr int TR = TWO ? 2 * kRows : kRows;  // query rows of a tile
     constexpr int kPageBytes = kPage * D;
-    constexpr int kStage = 4 * kPageBytes;        // two pages of k, two of v
-    constexpr int kQ = 2 * kRows * D;             // a stream's query digits
+    constexpr int kStage = 2 * kPageBytes;       // two pages of k, or of v
+    constexpr int kQ = 2 * kRows * D;            // a stream's query digits
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *qbuf = smem + NS * kStage;
+    uint8_t *kbuf = smem, *vbuf = kbuf + kKStages * kStage, *fbuf = vbuf + kVStages * kStage, *qbuf = fbuf + 2 * 2 * kStage;
     Control *ct = reinterpret_cast<Control *>(qbuf + (TWO ? 2 : 1) * kQ);
     Seqs &sq = *reinterpret_cast<Seqs *>(reinterpret_cast<uint8_t *>(ct) + sizeof(Control));
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const KvParams &c = p.c;
     const int G = c.q_heads / c.kv_heads;
+    auto aborted = [&] { return *reinterpret_cast<volatile int *>(&ct->abort) != 0; };
 
     if (tid == 0) {
         ct->abort = 0;
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&ct->full[i], 1);
-            mbar_init(&ct->empty[i], TWO ? 2 : 1);
+        const int streams = TWO ? 2 : 1;  // that use a stage
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(&ct->k_full[i], 1);
+            mbar_init(&ct->k_empty[i], streams);
         }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&ct->v_full[i], 1);
+            mbar_init(&ct->v_empty[i], 128);
+        }
+        for (int i = 0; i < kScales; ++i) mbar_init(&ct->sc_full[i], 1);
         mbar_init(&ct->q_ready, kConsumers);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&ct->f_full[s], 128);
+            mbar_init(&ct->f_empty[s], streams);
             mbar_init(&ct->s_ready[s], 1);
-            mbar_init(&ct->p_ready[s], kStream);
+            mbar_init(&ct->p_ready[s], kRows);
             mbar_init(&ct->o_ready[s], 1);
             mbar_init(&ct->drained[s], 1);
         }
@@ -211,16 +256,49 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
     if (static_cast<int>(blockIdx.x) >= blocks) return;
     const long long u0 = block_start(U, blocks, blockIdx.x), u1 = block_start(U, blocks, blockIdx.x + 1);
-    constexpr int kProducer = kConsumers / 32, kIssuer = kProducer + 1;  // warps
+    constexpr int kConverter = kConsumers / 32, kProducer = kConverter + 4, kIssuer = kProducer + 1;  // first warps
     if (wid == kIssuer) tc_alloc(&ct->tmem, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ct->tmem;
 
-    if (wid >= kProducer) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        if (wid == kProducer) {
+    if (wid >= kConverter) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (wid < kProducer) {
+            // ---- v's codes to fp16: rows of a head dim, 64 tokens of a page (128 bytes)
+            const int t = tid - kConsumers;
+            int it = 0;
+            for (long long u = u0; u < u1;) {
+                const Segment s = locate(sq, c.B, G, TR, u, u1);
+                const int end = it + (s.pe - s.p0 + 1) / 2;
+                for (; it < end; ++it) {
+                    const int vs = it % kVStages, f = it & 1;
+                    wait_or_abort(&ct->v_full[vs], (it / kVStages) & 1, p, &ct->abort);
+                    if (it >= 2) wait_or_abort(&ct->f_empty[f], (it / 2 - 1) & 1, p, &ct->abort);
+                    __syncwarp();
+                    const uint8_t *src = vbuf + vs * kStage;
+                    uint8_t *dst = fbuf + f * 2 * kStage;
+#pragma unroll 4
+                    for (int i = t; i < kStage / 16; i += 128) {  // 16 codes: granule i % 4 of row i / 4
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
+                        uint32_t h[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            h[2 * j] = e4m3x2_to_f16x2(static_cast<uint16_t>(u4w(w, j)));
+                            h[2 * j + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(u4w(w, j) >> 16));
+                        }
+                        const int row = i >> 2, gr = 2 * (i & 3);
+                        *reinterpret_cast<uint4 *>(dst + row * 128 + ((gr ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4 *>(dst + row * 128 + (((gr + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(&ct->f_full[f]);
+                    mbar_arrive(&ct->v_empty[vs]);
+                }
+                u += s.p1 - s.p0;
+            }
+        } else if (wid == kProducer) {
             // ---- producer: two pages a stage; an odd last page comes twice (the
             // second copy is behind every row's mask)
             int it = 0;
@@ -231,30 +309,38 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     const PageInfo pi = load_pages(c, s, pb);
                     const int m = min(32, s.pe - pb);
                     for (int i = 0; i < m; i += 2, ++it) {
-                        const int st = it % NS;
+                        const int ks = it % kKStages, vs = it % kVStages, sc = it % kScales;
                         int pid[2];
-                        float ks[2], vs[2];
+                        float pks[2], pvs[2];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const int src = min(i + x, m - 1);
                             pid[x] = __shfl_sync(0xffffffffu, pi.id, src);
-                            ks[x] = __shfl_sync(0xffffffffu, pi.ks, src);
-                            vs[x] = __shfl_sync(0xffffffffu, pi.vs, src);
+                            pks[x] = __shfl_sync(0xffffffffu, pi.ks, src);
+                            pvs[x] = __shfl_sync(0xffffffffu, pi.vs, src);
                         }
                         if (lane == 0) {
-                            if (it >= NS) wait_or_abort(&ct->empty[st], (it / NS - 1) & 1, p, &ct->abort);
-                            if (*reinterpret_cast<volatile int *>(&ct->abort) == 0) {
-                                mbar_expect_tx(&ct->full[st], kStage);
+                            // a page out of range is masked; page 0 stands in for its codes
+                            const int ph0 = max(pid[0], 0) * c.kv_heads + s.h, ph1 = max(pid[1], 0) * c.kv_heads + s.h;
+                            if (it >= kKStages) wait_or_abort(&ct->k_empty[ks], (it / kKStages - 1) & 1, p, &ct->abort);
+                            if (!aborted()) {
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
-                                    ct->ks[st][x] = ks[x];
-                                    ct->vs[st][x] = vs[x];
-                                    // a page out of range is masked; page 0 stands in for its codes
-                                    const int ph = max(pid[x], 0) * c.kv_heads + s.h;
-                                    uint8_t *dst = smem + st * kStage + x * kPageBytes;
-                                    tma2d(dst, &c.tm_k, 0, ph * kPage, &ct->full[st], pol);
-                                    tma2d(dst + 2 * kPageBytes, &c.tm_v, 0, ph * D, &ct->full[st], pol);
+                                    ct->ks[sc][x] = pks[x];
+                                    ct->vs[sc][x] = pvs[x];
                                 }
+                                mbar_arrive(&ct->sc_full[sc]);
+                                uint8_t *dst = kbuf + ks * kStage;
+                                mbar_expect_tx(&ct->k_full[ks], kStage);
+                                tma2d(dst, &c.tm_k, 0, ph0 * kPage, &ct->k_full[ks], pol);
+                                tma2d(dst + kPageBytes, &c.tm_k, 0, ph1 * kPage, &ct->k_full[ks], pol);
+                            }
+                            if (it >= kVStages) wait_or_abort(&ct->v_empty[vs], (it / kVStages - 1) & 1, p, &ct->abort);
+                            if (!aborted()) {
+                                uint8_t *dst = vbuf + vs * kStage;
+                                mbar_expect_tx(&ct->v_full[vs], kStage);
+                                bulk_g2s(dst, c.v + static_cast<size_t>(ph0) * kPageBytes, kPageBytes, &ct->v_full[vs], pol);
+                                bulk_g2s(dst + kPageBytes, c.v + static_cast<size_t>(ph1) * kPageBytes, kPageBytes, &ct->v_full[vs], pol);
                             }
                         }
                         __syncwarp();
@@ -262,19 +348,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 }
                 u += s.p1 - s.p0;
             }
-            if (lane == 0 && *reinterpret_cast<volatile int *>(&ct->abort)) {
+            if (lane == 0 && aborted()) {
                 // no block ends with a copy into its shared memory in flight
                 const uint64_t t0 = gtimer();
-                for (int j = max(it - NS, 0); j < it; ++j)
-                    while (!mbar_test(&ct->full[j % NS], (j / NS) & 1) &&
-                           static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
+                auto over = [&] { return static_cast<long long>(gtimer() - t0) >= p.timeout_ns; };
+                for (int j = max(it - kKStages, 0); j < it; ++j)
+                    while (!mbar_test(&ct->k_full[j % kKStages], (j / kKStages) & 1) && !over()) {
+                    }
+                for (int j = max(it - kVStages, 0); j < it; ++j)
+                    while (!mbar_test(&ct->v_full[j % kVStages], (j / kVStages) & 1) && !over()) {
                     }
             }
         } else if (wid == kIssuer || wid == kIssuer + 1) {
             // ---- MMA issue: a thread for each stream (its warp finds the segments), so
             // that a stream waits only for its own
             const int x = wid - kIssuer;
-            const uint32_t idesc_s = f8_idesc(kKeys), idesc_o = f8_idesc(D);
+            const uint32_t idesc_s = mma_idesc(kKeys), idesc_o = mma_idesc(D);
             const uint32_t sd = tmem + 256 * x, od = sd + 128;
             int base = 0, nseg = 0;  // stages before the segment; segments so far
             uint32_t sn = 0;         // steps so far
@@ -288,12 +377,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 tc_fence_after();
                 const uint32_t qa = smem_u32(qbuf) + (TWO ? x * kQ : 0);
                 for (int i = 0; i < steps; ++i, ++sn) {
-                    const int it = base + (TWO ? i : 2 * i + x), st = it % NS;
-                    const uint32_t ka = smem_u32(smem + st * kStage), va = ka + 2 * kPageBytes;
-                    wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);
+                    const int it = base + (TWO ? i : 2 * i + x), ks = it % kKStages, f = it & 1;
+                    const uint32_t ka = smem_u32(kbuf + ks * kStage), fa = smem_u32(fbuf + f * 2 * kStage);
+                    wait_or_abort(&ct->k_full[ks], (it / kKStages) & 1, p, &ct->abort);
                     // the scores take the place of the last step's weights
                     if (i > 0) wait_or_abort(&ct->o_ready[x], (sn - 1) & 1, p, &ct->abort);
-                    if (*reinterpret_cast<volatile int *>(&ct->abort)) continue;
+                    if (aborted()) continue;
                     tc_fence_after();
 #pragma unroll
                     for (int dg = 0; dg < 2; ++dg)
@@ -304,21 +393,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                                    idesc_s, dg + k > 0);
                         }
                     tc_commit(&ct->s_ready[x]);
+                    tc_commit(&ct->k_empty[ks]);
+                    wait_or_abort(&ct->f_full[f], (it / 2) & 1, p, &ct->abort);
                     wait_or_abort(&ct->p_ready[x], sn & 1, p, &ct->abort);
-                    if (*reinterpret_cast<volatile int *>(&ct->abort)) continue;
+                    if (aborted()) continue;
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 32 tokens each: two of each page
-#pragma unroll
-                        for (int dg = 0; dg < 2; ++dg)
-                            mma_f8_ts(od, sd + 16 * k + 8 * dg, sw64_desc(va + (k >> 1) * kPageBytes + 32 * (k & 1)), idesc_o,
-                                      i + k + dg > 0);
+                    for (int k = 0; k < 8; ++k)  // 16 tokens each: four of each page
+                        mma_f16_ts(od, sd + 8 * k, sw128_desc(fa + (k >> 2) * 2 * kPageBytes + 32 * (k & 3)), idesc_o, i + k > 0);
                     tc_commit(&ct->o_ready[x]);
-                    tc_commit(&ct->empty[st]);
+                    tc_commit(&ct->f_empty[f]);
                 }
                 base += stages;
             }
-            if (lane == 0 && *reinterpret_cast<volatile int *>(&ct->abort)) {
+            if (lane == 0 && aborted()) {
                 // no block ends with products in flight
                 tc_commit(&ct->drained[x]);
                 const uint64_t t0 = gtimer();
@@ -327,12 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             }
         }
     } else {
-        // ---- softmax: stream x, thread pairs (in two warpgroups) share a row; page y
+        // ---- softmax: stream x, a thread a row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
-        const int x = wid >> 3, y = (wid >> 2) & 1, row = tid & (kRows - 1);
+        const int x = wid >> 2, row = tid & (kRows - 1);
         const uint32_t lanes = static_cast<uint32_t>(wid & 3) << 21;  // this warp's tensor-memory lanes
         const uint32_t ts = tmem + 256 * x + lanes, to = ts + 128;
-        auto stream_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(2 + x), "n"(kStream) : "memory"); };
         int base = 0;
         uint32_t sn = 0, on[2] = {0, 0};  // this stream's steps so far; both streams'
         for (long long u = u0; u < u1;) {
@@ -343,99 +430,112 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const int row0 = s.tile * TR + (TWO ? kRows * x : 0);  // of the stream
             // queries: two neighbouring threads a row
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // both streams are done with the last
-            if (TWO || x == 0) {
-                const int qr = (tid & (kStream - 1)) >> 1, r = row0 + qr;
-                const float f = put_query<D>(qbuf + (TWO ? x * kQ : 0), qr, tid & 1,
+            for (int part = 0; part < (TWO ? 2 : 1); ++part) {
+                const int qr = 64 * (TWO ? part : x) + (row >> 1), r = row0 + qr;
+                const float f = put_query<D>(qbuf + (TWO ? x * kQ : 0), qr, row & 1,
                                              p.q + static_cast<long long>(q0 + r / G) * p.q_stride + (s.h * G + r % G) * D,
                                              r < rows, p.scale_log2);
-                if ((tid & 1) == 0) ct->qs[TWO ? x : 0][qr] = f;
+                if ((row & 1) == 0) ct->qs[TWO ? x : 0][qr] = f;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             mbar_arrive(&ct->q_ready);
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             const int r = row0 + row;
-            const float qs = ct->qs[TWO ? x : 0][row];
             const int sees = r < rows ? row_sees(len, n, G, r) : 0;
+            const float qs = sees > 0 ? ct->qs[TWO ? x : 0][row] : 0.f;
             const int tile_sees = row_sees(len, n, G, row0);  // the least of the stream's rows
 
             float ref = -INFINITY, l = 0.f;
             for (int i = 0; i < steps; ++i) {
-                const int it = base + (TWO ? i : 2 * i + x), st = it % NS;
-                wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);  // the page's scales
+                const int it = base + (TWO ? i : 2 * i + x), sc = it % kScales;
+                wait_or_abort(&ct->sc_full[sc], (it / kScales) & 1, p, &ct->abort);
                 wait_or_abort(&ct->s_ready[x], (sn + i) & 1, p, &ct->abort);
                 __syncwarp();
                 tc_fence_after();
-                // the row's scores of this page
-                float a[64];
-                tc_ld32(ts + 64 * y, *reinterpret_cast<float(*)[32]>(a));
-                tc_ld32(ts + 64 * y + 32, *reinterpret_cast<float(*)[32]>(a + 32));
-                const float ks = ct->ks[st][y], vs = ct->vs[st][y];
-                const int pg = s.p0 + 2 * (it - base) + y;
-                const bool none = ks < 0.f || pg >= s.pe;  // no such page
-                const float fs = qs * ks;
+                float a[4][32];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) tc_ld32(ts + 32 * h, a[h]);
+                const float2 ks = *reinterpret_cast<const float2 *>(ct->ks[sc]), vs = *reinterpret_cast<const float2 *>(ct->vs[sc]);
+                const int pg = s.p0 + 2 * (it - base);
+                const bool none0 = ks.x < 0.f, none1 = ks.y < 0.f || pg + 1 >= s.pe;  // no such page
                 tc_wait_ld();
-                if (none || (pg + 1) * kPage > tile_sees) {
-                    const int lim = none ? 0 : sees - pg * kPage;
+                if (none0 || none1 || (pg + 2) * kPage > tile_sees) {
+                    const int lim0 = none0 ? 0 : sees - pg * kPage, lim1 = none1 ? 0 : sees - (pg + 1) * kPage;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (j >= lim) a[j] = -INFINITY;
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * (h & 1) + j >= (h < 2 ? lim0 : lim1)) a[h][j] = -INFINITY;
                 }
-                // their largest, in log2 units (a row's factor is not negative), with the other page's
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // the largest, in log2 units (a row's factor is not negative)
+                float fs[2] = {qs * ks.x, qs * ks.y};
 #pragma unroll
-                for (int j = 0; j < 64; j += 8)
+                for (int y = 0; y < 2; ++y)
+                    if (fs[y] == 0.f) fs[y] = 1.17549435e-38f;  // masked scores (-inf) stay what they are
+                const float lv[2] = {scale_log2(vs.x), scale_log2(vs.y)};
+                float mx = -INFINITY;
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) m4[z] = fmaxf(m4[z], fmaxf(a[j + z], a[j + 4 + z]));
-                const float mr = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                float mx = mr > -INFINITY ? mr * fs + scale_log2(vs) : -INFINITY;
-                ct->mx[x][y][row] = mx;
-                tc_fence_before();
-                stream_sync();  // (the weights overwrite the other page's scores: they have been read)
-                tc_fence_after();
-                mx = fmaxf(mx, ct->mx[x][y ^ 1][row]);
+                for (int y = 0; y < 2; ++y) {
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int j = 0; j < 64; j += 8)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float *w = &a[2 * y + (j >> 5)][j & 31];
+                            m4[z] = fmaxf(m4[z], fmaxf(w[z], w[z + 4]));
+                        }
+                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    if (m > -INFINITY) mx = fmaxf(mx, fmaf(m, fs[y], lv[y]));
+                }
                 const bool move = mx > ref + kSlack;  // (ref = -inf: as soon as anything is seen)
                 if (__any_sync(0xffffffffu, move)) {
                     const float nref = move ? mx : ref;
                     const float f = move ? ex2(ref - nref) : 1.f;
                     l *= f;
                     ref = nref;
-                    if (i > 0) {  // this thread's half of the row's accumulators
+                    if (i > 0) {
                         wait_or_abort(&ct->o_ready[x], (sn + i - 1) & 1, p, &ct->abort);
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
-                        for (int h = 0; h < D / 32; ++h) {
+                        for (int h = 0; h < D / 16; ++h) {
                             float v[16];
                             uint32_t b[16];
-                            tc_ld16(to + (D / 2) * y + 16 * h, v);
+                            tc_ld16(to + 16 * h, v);
                             tc_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; ++j) b[j] = __float_as_uint(v[j] * f);
-                            tc_st16(to + (D / 2) * y + 16 * h, b);
+                            tc_st16(to + 16 * h, b);
                         }
                     }
                 }
-                // 64 w vs as digits, 32 tokens at a time; w's sum from theirs
-                const float pv = fmaxf(vs, 0x1p-64f) * kGain;
-                const float add = __log2f(pv) - (ref == -INFINITY ? 0.f : ref);
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                // 64 w vs in fp16, over the scores; w's sum from the unrounded values
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int y = 0; y < 2; ++y) {
+                    const float pv = fmaxf(y ? vs.y : vs.x, 0x1p-64f) * kGain;
+                    const float add = __log2f(pv) - (ref == -INFINITY ? 0.f : ref);
+                    const uint64_t f2 = pack2(fs[y], fs[y]), add2v = pack2(add, add);
+                    uint64_t l2[2] = {0, 0};
 #pragma unroll
-                    for (int j = 32 * h; j < 32 * h + 32; ++j) {
-                        a[j] = ex2(fmaf(a[j], fs, add));
-                        l4[j & 3] += a[j];
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int h = 2 * y + hh;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float e0, e1;
+                            unpack2(fma2(pack2(a[h][2 * j], a[h][2 * j + 1]), f2, add2v), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            l2[j & 1] = add2(l2[j & 1], pack2(e0, e1));
+                            w[j] = cvt_f16x2(e0, e1);
+                        }
+                        tc_st16(ts + 16 * h, w);
                     }
-                    uint32_t dg[16];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float *w = a + 32 * h + 4 * j;
-                        digits4(w[0], w[1], w[2], w[3], dg[j], dg[8 + j]);
-                    }
-                    tc_st16(ts + 32 * y + 16 * h, dg);
+                    float e0, e1;
+                    unpack2(add2(l2[0], l2[1]), e0, e1);
+                    l += (e0 + e1) * (1.f / pv);
                 }
-                l += ((l4[0] + l4[1]) + (l4[2] + l4[3])) * (1.f / pv);
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&ct->p_ready[x]);
@@ -445,35 +545,35 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             on[1] += TWO ? stages : stages / 2;
 
             // ---- the result: o / 64 in tensor memory, references and sums
-            if (y == 0) ct->m[x][row] = ref;
-            ct->l[x][y][row] = l;
-            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             const bool have0 = stages > 0, have1 = !TWO && stages > 1;
             const int x0 = TWO ? x : 0;
-            if (have0) wait_or_abort(&ct->o_ready[x0], (on[x0] - 1) & 1, p, &ct->abort);
-            if (have1) wait_or_abort(&ct->o_ready[1], (on[1] - 1) & 1, p, &ct->abort);
-            __syncwarp();
-            tc_fence_after();
-            float f0 = 1.f, f1 = 0.f, msum = ref, lsum = ct->l[x0][0][row] + ct->l[x0][1][row];
+            float f0 = 1.f, f1 = 0.f, msum = ref, lsum = l;
             if (!TWO) {  // the streams' together
+                ct->m[x][row] = ref;
+                ct->l[x][row] = l;
+                asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
                 const float m0 = ct->m[0][row], m1 = ct->m[1][row];
                 msum = fmaxf(m0, m1);
                 const float mref = msum == -INFINITY ? 0.f : msum;
                 f0 = ex2(m0 - mref);
                 f1 = ex2(m1 - mref);
-                lsum = lsum * f0 + (ct->l[1][0][row] + ct->l[1][1][row]) * f1;
+                lsum = ct->l[0][row] * f0 + ct->l[1][row] * f1;
             }
+            if (have0) wait_or_abort(&ct->o_ready[x0], (on[x0] - 1) & 1, p, &ct->abort);
+            if (have1) wait_or_abort(&ct->o_ready[1], (on[1] - 1) & 1, p, &ct->abort);
+            __syncwarp();
+            tc_fence_after();
             float *part = part_slot(p, blockIdx.x, s.p0 == 0);
             const int rr = TWO ? kRows * x + row : row;
-            if (!s.whole() && y == 0 && (TWO || x == 0)) {
+            if (!s.whole() && (TWO || x == 0)) {
                 part[rr] = msum;
                 part[TR + rr] = lsum;
             }
             const float inv = inv_sum(kGain, lsum);
             uint16_t *orow = out_row(p, q0, s.h, G, min(r, rows - 1));
-            constexpr int kCols = TWO ? D / 2 : D / 4;  // of this thread
-            const int col0 = kCols * (TWO ? y : 2 * x + y);
-#pragma unroll 1
+            constexpr int kCols = TWO ? D : D / 2;  // of this thread
+            const int col0 = TWO ? 0 : kCols * x;
+#pragma unroll 2
             for (int col = col0; col < col0 + kCols; col += 16) {
                 float v[16], w[16];
 #pragma unroll
@@ -513,28 +613,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 }
 
 template <int D, bool TWO>
-cudaError_t launch_one(const AttendParams &p, int grid, int smem_optin, cudaStream_t st)
+cudaError_t launch_one(const AttendParams &p, int grid, cudaStream_t st)
 {
-    constexpr int kStage = 4 * kPage * D;
-    const int fixed = 1024 + static_cast<int>(sizeof(Control) + sizeof(Seqs)) + (TWO ? 2 : 1) * 2 * kRows * D;
-    const int ns = std::min(kMaxStages, (smem_optin - fixed) / kStage);
-    const int smem = fixed + ns * kStage;
+    // k, v, v in fp16 (twice as many bytes, two buffers), query digits
+    constexpr int smem = 1024 + 2 * kPage * D * (kKStages + kVStages + 4) + (TWO ? 2 : 1) * 2 * kRows * D +
+                         static_cast<int>(sizeof(Control) + sizeof(Seqs));
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
     auto *fn = moe_kv_attend_tc_kernel<D, TWO>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     LaunchCfg l(dim3(grid), dim3(kThreads), smem, st);
-    return cudaLaunchKernelEx(&l.cfg, fn, p, ns);
+    return cudaLaunchKernelEx(&l.cfg, fn, p);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend_tc(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st)
+cudaError_t launch_kv_attend_tc(const AttendParams &p, int tile_rows, int num_sms, cudaStream_t st)
 {
     if (p.c.D == 128)
-        return tile_rows == 256 ? launch_one<128, true>(p, num_sms, smem_optin, st)
-                                : launch_one<128, false>(p, num_sms, smem_optin, st);
-    return tile_rows == 256 ? launch_one<64, true>(p, num_sms, smem_optin, st)
-                            : launch_one<64, false>(p, num_sms, smem_optin, st);
+        return tile_rows == 256 ? launch_one<128, true>(p, num_sms, st) : launch_one<128, false>(p, num_sms, st);
+    return tile_rows == 256 ? launch_one<64, true>(p, num_sms, st) : launch_one<64, false>(p, num_sms, st);
 }
 
 }  // namespace moe

@@ -18,7 +18,7 @@ struct moe_kv {
     moe_kv_desc d;
     int device = 0, num_sms = 0, smem_optin = 0;
     long long timeout_ns = 0;
-    CUtensorMap tm_k{}, tm_v{};
+    CUtensorMap tm_k{};
     size_t off_count = 0, off_part = 0, ws_bytes = 0;
 };
 
@@ -109,7 +109,7 @@ moe::KvParams kv_params(const moe_kv *kv, const moe_kv_batch *b, void *ws)
 {
     moe::KvParams c{};
     const moe_kv_desc &d = kv->d;
-    c.tm_k = kv->tm_k, c.tm_v = kv->tm_v;
+    c.tm_k = kv->tm_k;
     c.k = d.k_dev, c.v = d.v_dev, c.ks = d.k_scale_dev, c.vs = d.v_scale_dev, c.rope = d.rope_dev;
     c.n_pages = d.n_pages, c.q_heads = d.q_heads, c.kv_heads = d.kv_heads, c.D = d.head_dim;
     c.rot_dim = d.rot_dim, c.rot_inter = d.rot_interleaved, c.rope_positions = d.rope_positions;
@@ -214,8 +214,7 @@ moe_status_t moe_kv_create(const moe_kv_desc *desc, moe_kv_t *out)
     kv->smem_optin = dev.optin;
     kv->timeout_ns = moe::wait_limit_ns();
     const uint64_t ph = static_cast<uint64_t>(d.n_pages) * d.kv_heads;
-    CUresult r = moe::encode_rows(&kv->tm_k, d.k_dev, ph * MOE_KV_PAGE, d.head_dim, d.head_dim, MOE_KV_PAGE, d.head_dim);
-    if (r == CUDA_SUCCESS) r = moe::encode_rows(&kv->tm_v, d.v_dev, ph * d.head_dim, MOE_KV_PAGE, MOE_KV_PAGE, d.head_dim, MOE_KV_PAGE);
+    const CUresult r = moe::encode_rows(&kv->tm_k, d.k_dev, ph * MOE_KV_PAGE, d.head_dim, d.head_dim, MOE_KV_PAGE, d.head_dim);
     if (r != CUDA_SUCCESS) {
         delete kv;
         return fail(MOE_ERR_CUDA, "tensor-map encoding failed (CUresult %d)", static_cast<int>(r));
@@ -292,8 +291,10 @@ moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, flo
                         reinterpret_cast<float *>(ws + kv->off_part), kv->timeout_ns};
     moe::WsTicket tk;
     if ((st = moe::ws_claim(ws_dev, static_cast<cudaStream_t>(stream), tk)) != MOE_OK) return st;
-    const cudaError_t e = (tile_rows <= 16 ? moe::launch_kv_attend_rows : moe::launch_kv_attend_tc)(
-        p, tile_rows, kv->num_sms, kv->smem_optin, static_cast<cudaStream_t>(stream));
+    const cudaError_t e =
+        tile_rows <= 16
+            ? moe::launch_kv_attend_rows(p, tile_rows, kv->num_sms, kv->smem_optin, static_cast<cudaStream_t>(stream))
+            : moe::launch_kv_attend_tc(p, tile_rows, kv->num_sms, static_cast<cudaStream_t>(stream));
     moe::ws_release(tk, e == cudaSuccess);
     return launched(e, "attention launch");
 }

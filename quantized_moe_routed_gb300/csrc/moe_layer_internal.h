@@ -39,9 +39,7 @@ cudaError_t launch_linear(const LinearParams &p, int num_sms, cudaStream_t st);
 
 // The cache's pages, and one step's sequences (fields as in moe_layer.h).
 struct KvParams {
-    // a page's k as 64 rows of head_dim bytes, its v as head_dim rows of 64,
-    // swizzled by the row's length (128 or 64 bytes)
-    CUtensorMap tm_k, tm_v;
+    CUtensorMap tm_k;  // a page's k as 64 rows of head_dim bytes, swizzled over the row (128 or 64 bytes)
     uint8_t *k, *v;
     float *ks, *vs;
     const float *rope;
@@ -77,6 +75,6 @@ constexpr int kAttendMaxRows = 256;  // query rows of the largest tile
 __host__ __device__ inline size_t attend_part_floats(int D) { return static_cast<size_t>(kAttendMaxRows) * (D + 2); }
 cudaError_t launch_kv_attend_rows(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st);
 // moe_kv_attend_tc.cu: tiles of 128 or 256 rows
-cudaError_t launch_kv_attend_tc(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st);
+cudaError_t launch_kv_attend_tc(const AttendParams &p, int tile_rows, int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -164,6 +164,20 @@ def test_attend_rows_that_see_nothing_are_zero(n, Hq):
     _check_attend(step, bufs, q, out, 1 / math.sqrt(128))
 
 
+@pytest.mark.parametrize("n", [1, 9, 40, 70])
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1.5])
+def test_attend_softmax_scale(n, scale):
+    """No scale at all (equal weights), a negative one, one that leaves a few weights."""
+    step = Step([n, n], [200, n], seed=12)
+    bufs = _pool(step, 2, 128, seed=12)
+    _stale(step, bufs[0])
+    q = torch.randn((2 * n, 8, 128), generator=torch.Generator().manual_seed(1)).bfloat16()
+    cache = _cache(bufs, 8, 2, 128)
+    ws = cache.new_workspace()
+    out = cache.attend(q.to(DEV), *step.dev(), ws, max_q=n, scale=scale)
+    _check_attend(step, bufs, q, out, scale)
+
+
 @pytest.mark.parametrize("n", [1, 6, 40])
 def test_attend_scales_of_very_different_size(n):
     """Pages whose v differ by 2^50, scores up to large ones, a custom scale."""
