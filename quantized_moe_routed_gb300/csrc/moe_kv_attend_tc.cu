@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const Segment s = locate(sq, c.B, G, TR, u, u1);
             const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b];
             const int stages = (s.pe - s.p0 + 1) / 2;
-            const int steps = TWO ? stages : (stages + 1 - x) / 2;
+            const int steps = TWO ? stages : (stages + 1 - x) / 2, others = TWO ? stages : (stages + x) / 2;
             const int row0 = s.tile * TR + (TWO ? kRows * x : 0);  // of the stream
             // queries: two neighbouring threads a row
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // both streams are done with the last
@@ -451,6 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 const int it = base + (TWO ? i : 2 * i + x), sc = it % kScales;
                 wait_or_abort(&ct->sc_full[sc], (it / kScales) & 1, p, &ct->abort);
                 wait_or_abort(&ct->s_ready[x], (sn + i) & 1, p, &ct->abort);
+                // the streams' softmax steps take turns (0, 1, 0, 1, ..), so that one's
+                // products run during the other's softmax and not beside the other's
+                if (x == 1 || i > 0) asm volatile("bar.sync %0, %1;" ::"r"(2 + x), "n"(kConsumers) : "memory");
                 __syncwarp();
                 tc_fence_after();
                 float a[4][32];
@@ -536,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     unpack2(add2(l2[0], l2[1]), e0, e1);
                     l += (e0 + e1) * (1.f / pv);
                 }
+                if (i + x < others) asm volatile("bar.arrive %0, %1;" ::"r"(3 - x), "n"(kConsumers) : "memory");
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&ct->p_ready[x]);
