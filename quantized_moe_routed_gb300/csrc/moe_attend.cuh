@@ -26,17 +26,16 @@ struct Seqs {
 // waiting, so that every warp still reaches the block's barriers.
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, const AttendParams &p, int *abort_flag)
 {
-    if (mbar_test(bar, parity)) return;
-    const uint64_t t0 = gtimer();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_test(bar, parity)) return;
-        if ((it & 31u) == 0) {
-            if (*reinterpret_cast<volatile int *>(abort_flag)) return;
-            if (static_cast<long long>(gtimer() - t0) > p.timeout_ns) {
-                atomicOr(p.c.ctrl + 2, kErrTimeout);
-                *reinterpret_cast<volatile int *>(abort_flag) = 1;
-                return;
-            }
+    uint64_t t0 = 0;  // (reading the timer takes long: not before many tries have failed)
+    for (uint32_t it = 1; !mbar_test(bar, parity); ++it) {
+        if ((it & 31u) != 0) continue;
+        if (*reinterpret_cast<volatile int *>(abort_flag)) return;
+        const uint64_t t = gtimer();
+        if (t0 == 0) t0 = t;
+        if (static_cast<long long>(t - t0) > p.timeout_ns) {
+            atomicOr(p.c.ctrl + 2, kErrTimeout);
+            *reinterpret_cast<volatile int *>(abort_flag) = 1;
+            return;
         }
     }
 }

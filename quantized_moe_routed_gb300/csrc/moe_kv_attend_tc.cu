@@ -7,7 +7,7 @@
 // Both products run on the tensor cores (tcgen05.mma), their accumulators in
 // tensor memory:
 //
-//  * S[128 rows x 128 tokens] = Q K^T, kind::f8f6f4 on the cache's E4M3 codes as TMA
+//  * S[128 rows x 64 tokens of a page] = Q K^T, kind::f8f6f4 on the cache's E4M3 codes as TMA
 //    brings them: q enters as two E4M3 digits, hi + lo, after a power-of-two
 //    prescale of the row (largest magnitude into [128, 256)): 8 significant bits
 //    are two digits of 4, so the sum is exact down to 2^-10 of the row's
@@ -24,11 +24,14 @@
 // tensor memory are rescaled rarely.
 //
 // A block runs two streams, each with a warpgroup for the softmax (a thread a
-// row), a thread that issues its MMAs, and its own S / P and O in tensor memory,
-// so that one stream's softmax and the other's products overlap.  With TWO, the
-// streams are two row tiles that share the pages; otherwise they are the even
-// and the odd page pairs of one row tile, joined at the end.  One warp brings
-// pages, two a stage; a warpgroup converts v.
+// row), a thread that issues its MMAs, and in tensor memory its own O and two S / P
+// buffers: the scores of the next page are computed while the softmax works on
+// this one's, so that it never waits for the chain from its weights over P V to
+// the next scores (with one buffer of 128 tokens that chain, mostly latencies, took
+// longer than the softmax: 580 against ~XXX us for 2048 x 16384, 32 heads).
+// With TWO, the streams are two row tiles that share the pages; otherwise they
+// are the even and the odd pages of one row tile, joined at the end.  One warp
+// brings pages; a warpgroup converts v.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -52,40 +55,49 @@ constexpr int kThreads = kConsumers + 256;  // and a warpgroup that converts v, 
 // Registers a thread of the two kinds keeps: 256 * 200 + 256 * 56 = 65536, what the
 // block is launched with (512 threads of 128).
 constexpr int kConsumerRegs = 200, kOtherRegs = 56;
-constexpr int kKeys = 2 * kPage; // tokens of a stage
 constexpr float kGain = 64.f;    // of the weights
 constexpr float kSlack = 8.f;    // how far a step may exceed the reference (64 * 2^8 is inside fp16)
-constexpr int kTmemCols = 512;   // stream s: S / P at 256 s, O at 256 s + 128
-constexpr int kKStages = 3, kVStages = 2;
-constexpr int kScales = 8;       // stages whose scales are kept: more than any warp lags behind the producer
+constexpr int kTmemCols = 512;   // stream s: S / P buffer b at 256 s + 64 b, O at 256 s + 128
+constexpr int kKStages = 6, kVStages = 4, kFStages = 4;  // pages of k, of v, of v in fp16
+constexpr int kScales = 16;      // pages whose scales are kept: more than a softmax lags behind the producer (10)
 
 struct Control {
     uint64_t k_full[kKStages], k_empty[kKStages];   // codes of k
     uint64_t v_full[kVStages], v_empty[kVStages];   // codes of v
-    uint64_t f_full[2], f_empty[2];                 // v in fp16
+    uint64_t f_full[kFStages], f_empty[kFStages];   // v in fp16
     uint64_t sc_full[kScales];
-    uint64_t q_ready, s_ready[2], p_ready[2], o_ready[2], drained[2];
-    float ks[kScales][2], vs[kScales][2];  // scales of a stage's pages; ks < 0: no such page
+    uint64_t q_ready, s_ready[2][2], p_ready[2][2], o_ready[2], drained[2];  // [stream][buffer]
+    float ks[kScales], vs[kScales];        // a page's scales; ks < 0: no such page
     float qs[2][kRows];                    // each row's factor from digits to scores (log2 units)
     float m[2][kRows], l[2][kRows];        // the streams' references and sums, for joining them
     uint32_t tmem;
     int abort, last;
 };
 
+// Matrix descriptors of K-major tiles: rows of 128 bytes with the 128-byte swizzle,
+// 8-row groups 1024 bytes apart, or rows of 64 bytes with the 64-byte swizzle, groups
+// 512 bytes apart.  The high word is a constant, the low one holds the address, so
+// the next step along K is one addition (a lone issuing thread has nothing to
+// hide a longer computation behind).
+__host__ __device__ constexpr uint32_t desc_hi(int row) { return row == 128 ? (1024u >> 4) | (1u << 14) | (2u << 29) : (512u >> 4) | (1u << 14) | (4u << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+
 // D[128 x N] (+)= A B^T: E4M3 operands, both in shared memory
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+template <bool ADD>
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n}" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc),
+        "n"(ADD ? 1 : 0)
         : "memory");
 }
 // The same for fp16 operands, A in tensor memory.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t add)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(add)
         : "memory");
 }
 // Instruction descriptor: fp32 accumulator, E4M3 (kind::f8f6f4) or fp16 (kind::f16)
@@ -93,13 +105,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
 __device__ __forceinline__ uint32_t mma_idesc(int n)
 {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-}
-// Matrix descriptor: K-major rows of 64 bytes, 64-byte swizzle, 8-row groups
-// 512 bytes apart.
-__device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr)
-{
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(4) << 61);
 }
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&r)[32])
 {
@@ -214,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 {
     constexpr int TR = TWO ? 2 * kRows : kRows;  // query rows of a tile
     constexpr int kPageBytes = kPage * D;
-    constexpr int kStage = 2 * kPageBytes;       // two pages of k, or of v
     constexpr int kQ = 2 * kRows * D;            // a stream's query digits
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *kbuf = smem, *vbuf = kbuf + kKStages * kStage, *fbuf = vbuf + kVStages * kStage, *qbuf = fbuf + 2 * 2 * kStage;
+    uint8_t *kbuf = smem, *vbuf = kbuf + kKStages * kPageBytes, *fbuf = vbuf + kVStages * kPageBytes;
+    uint8_t *qbuf = fbuf + kFStages * 2 * kPageBytes;
     Control *ct = reinterpret_cast<Control *>(qbuf + (TWO ? 2 : 1) * kQ);
     Seqs &sq = *reinterpret_cast<Seqs *>(reinterpret_cast<uint8_t *>(ct) + sizeof(Control));
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 
     if (tid == 0) {
         ct->abort = 0;
-        const int streams = TWO ? 2 : 1;  // that use a stage
+        const int streams = TWO ? 2 : 1;  // that use a page
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(&ct->k_full[i], 1);
             mbar_init(&ct->k_empty[i], streams);
@@ -239,11 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
         }
         for (int i = 0; i < kScales; ++i) mbar_init(&ct->sc_full[i], 1);
         mbar_init(&ct->q_ready, kConsumers);
+        for (int i = 0; i < kFStages; ++i) {
+            mbar_init(&ct->f_full[i], 128);
+            mbar_init(&ct->f_empty[i], streams);
+        }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&ct->f_full[s], 128);
-            mbar_init(&ct->f_empty[s], streams);
-            mbar_init(&ct->s_ready[s], 1);
-            mbar_init(&ct->p_ready[s], kRows);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&ct->s_ready[s][b], 1);
+                mbar_init(&ct->p_ready[s][b], kRows);
+            }
             mbar_init(&ct->o_ready[s], 1);
             mbar_init(&ct->drained[s], 1);
         }
@@ -271,16 +280,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             int it = 0;
             for (long long u = u0; u < u1;) {
                 const Segment s = locate(sq, c.B, G, TR, u, u1);
-                const int end = it + (s.pe - s.p0 + 1) / 2;
+                const int end = it + s.pe - s.p0;
                 for (; it < end; ++it) {
-                    const int vs = it % kVStages, f = it & 1;
+                    const int vs = it % kVStages, f = it % kFStages;
                     wait_or_abort(&ct->v_full[vs], (it / kVStages) & 1, p, &ct->abort);
-                    if (it >= 2) wait_or_abort(&ct->f_empty[f], (it / 2 - 1) & 1, p, &ct->abort);
+                    if (it >= kFStages) wait_or_abort(&ct->f_empty[f], (it / kFStages - 1) & 1, p, &ct->abort);
                     __syncwarp();
-                    const uint8_t *src = vbuf + vs * kStage;
-                    uint8_t *dst = fbuf + f * 2 * kStage;
+                    const uint8_t *src = vbuf + vs * kPageBytes;
+                    uint8_t *dst = fbuf + f * 2 * kPageBytes;
 #pragma unroll 4
-                    for (int i = t; i < kStage / 16; i += 128) {  // 16 codes: granule i % 4 of row i / 4
+                    for (int i = t; i < kPageBytes / 16; i += 128) {  // 16 codes: granule i % 4 of row i / 4
                         const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
                         uint32_t h[8];
 #pragma unroll
@@ -299,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 u += s.p1 - s.p0;
             }
         } else if (wid == kProducer) {
-            // ---- producer: two pages a stage; an odd last page comes twice (the
-            // second copy is behind every row's mask)
+            // ---- producer
             int it = 0;
             const uint64_t pol = TWO ? policy_evict_last() : policy_evict_first();  // other tiles read the page too
             for (long long u = u0; u < u1;) {
@@ -308,39 +316,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 for (int pb = s.p0; pb < s.pe; pb += 32) {
                     const PageInfo pi = load_pages(c, s, pb);
                     const int m = min(32, s.pe - pb);
-                    for (int i = 0; i < m; i += 2, ++it) {
+                    for (int i = 0; i < m; ++i, ++it) {
                         const int ks = it % kKStages, vs = it % kVStages, sc = it % kScales;
-                        int pid[2];
-                        float pks[2], pvs[2];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int src = min(i + x, m - 1);
-                            pid[x] = __shfl_sync(0xffffffffu, pi.id, src);
-                            pks[x] = __shfl_sync(0xffffffffu, pi.ks, src);
-                            pvs[x] = __shfl_sync(0xffffffffu, pi.vs, src);
-                        }
+                        const int pid = __shfl_sync(0xffffffffu, pi.id, i);
+                        const float pks = __shfl_sync(0xffffffffu, pi.ks, i), pvs = __shfl_sync(0xffffffffu, pi.vs, i);
                         if (lane == 0) {
                             // a page out of range is masked; page 0 stands in for its codes
-                            const int ph0 = max(pid[0], 0) * c.kv_heads + s.h, ph1 = max(pid[1], 0) * c.kv_heads + s.h;
+                            const int ph = max(pid, 0) * c.kv_heads + s.h;
                             if (it >= kKStages) wait_or_abort(&ct->k_empty[ks], (it / kKStages - 1) & 1, p, &ct->abort);
                             if (!aborted()) {
-#pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    ct->ks[sc][x] = pks[x];
-                                    ct->vs[sc][x] = pvs[x];
-                                }
+                                ct->ks[sc] = pks;
+                                ct->vs[sc] = pvs;
                                 mbar_arrive(&ct->sc_full[sc]);
-                                uint8_t *dst = kbuf + ks * kStage;
-                                mbar_expect_tx(&ct->k_full[ks], kStage);
-                                tma2d(dst, &c.tm_k, 0, ph0 * kPage, &ct->k_full[ks], pol);
-                                tma2d(dst + kPageBytes, &c.tm_k, 0, ph1 * kPage, &ct->k_full[ks], pol);
+                                mbar_expect_tx(&ct->k_full[ks], kPageBytes);
+                                tma2d(kbuf + ks * kPageBytes, &c.tm_k, 0, ph * kPage, &ct->k_full[ks], pol);
                             }
                             if (it >= kVStages) wait_or_abort(&ct->v_empty[vs], (it / kVStages - 1) & 1, p, &ct->abort);
                             if (!aborted()) {
-                                uint8_t *dst = vbuf + vs * kStage;
-                                mbar_expect_tx(&ct->v_full[vs], kStage);
-                                bulk_g2s(dst, c.v + static_cast<size_t>(ph0) * kPageBytes, kPageBytes, &ct->v_full[vs], pol);
-                                bulk_g2s(dst + kPageBytes, c.v + static_cast<size_t>(ph1) * kPageBytes, kPageBytes, &ct->v_full[vs], pol);
+                                mbar_expect_tx(&ct->v_full[vs], kPageBytes);
+                                bulk_g2s(vbuf + vs * kPageBytes, c.v + static_cast<size_t>(ph) * kPageBytes, kPageBytes,
+                                         &ct->v_full[vs], pol);
                             }
                         }
                         __syncwarp();
@@ -363,48 +358,54 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             // ---- MMA issue: a thread for each stream (its warp finds the segments), so
             // that a stream waits only for its own
             const int x = wid - kIssuer;
-            const uint32_t idesc_s = mma_idesc(kKeys), idesc_o = mma_idesc(D);
+            const uint32_t idesc_s = mma_idesc(kPage), idesc_o = mma_idesc(D);
             const uint32_t sd = tmem + 256 * x, od = sd + 128;
-            int base = 0, nseg = 0;  // stages before the segment; segments so far
+            int base = 0, nseg = 0;  // pages before the segment; segments so far
             uint32_t sn = 0;         // steps so far
             for (long long u = u0; u < u1; ++nseg) {
                 const Segment s = locate(sq, c.B, G, TR, u, u1);
-                const int stages = (s.pe - s.p0 + 1) / 2, steps = TWO ? stages : (stages + 1 - x) / 2;
+                const int pages = s.pe - s.p0, steps = TWO ? pages : (pages + 1 - x) / 2;
                 u += s.p1 - s.p0;
                 __syncwarp();
                 if (lane != 0) continue;
                 wait_or_abort(&ct->q_ready, nseg & 1, p, &ct->abort);
                 tc_fence_after();
-                const uint32_t qa = smem_u32(qbuf) + (TWO ? x * kQ : 0);
-                for (int i = 0; i < steps; ++i, ++sn) {
-                    const int it = base + (TWO ? i : 2 * i + x), ks = it % kKStages, f = it & 1;
-                    const uint32_t ka = smem_u32(kbuf + ks * kStage), fa = smem_u32(fbuf + f * 2 * kStage);
+                const uint32_t qd = desc_lo(smem_u32(qbuf) + (TWO ? x * kQ : 0));
+                auto scores = [&](int i) {  // of step i, into buffer (sn + i) & 1
+                    const int it = base + (TWO ? i : 2 * i + x), ks = it % kKStages, b = (sn + i) & 1;
+                    const uint32_t kd = desc_lo(smem_u32(kbuf + ks * kPageBytes)), d = sd + 64 * b;
                     wait_or_abort(&ct->k_full[ks], (it / kKStages) & 1, p, &ct->abort);
-                    // the scores take the place of the last step's weights
-                    if (i > 0) wait_or_abort(&ct->o_ready[x], (sn - 1) & 1, p, &ct->abort);
-                    if (aborted()) continue;
+                    // they take the place of the weights of the step before the last
+                    if (i > 1) wait_or_abort(&ct->o_ready[x], (sn + i) & 1, p, &ct->abort);
+                    if (aborted()) return;
                     tc_fence_after();
+                    mma_f8<false>(d, qd, kd, desc_hi(D), idesc_s);
 #pragma unroll
-                    for (int dg = 0; dg < 2; ++dg)
+                    for (int k = 1; k < D / 32; ++k) mma_f8<true>(d, qd + 2 * k, kd + 2 * k, desc_hi(D), idesc_s);
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            const uint32_t a = qa + dg * (kRows * D) + 32 * k, b = ka + 32 * k;
-                            mma_f8(sd, D == 128 ? sw128_desc(a) : sw64_desc(a), D == 128 ? sw128_desc(b) : sw64_desc(b),
-                                   idesc_s, dg + k > 0);
-                        }
-                    tc_commit(&ct->s_ready[x]);
+                    for (int k = 0; k < D / 32; ++k)
+                        mma_f8<true>(d, qd + kRows * D / 16 + 2 * k, kd + 2 * k, desc_hi(D), idesc_s);
+                    tc_commit(&ct->s_ready[x][b]);
                     tc_commit(&ct->k_empty[ks]);
-                    wait_or_abort(&ct->f_full[f], (it / 2) & 1, p, &ct->abort);
-                    wait_or_abort(&ct->p_ready[x], sn & 1, p, &ct->abort);
+                };
+                if (steps > 0) scores(0);
+                if (steps > 1) scores(1);
+                for (int i = 0; i < steps; ++i) {
+                    const int it = base + (TWO ? i : 2 * i + x), f = it % kFStages, b = (sn + i) & 1;
+                    const uint32_t fd = desc_lo(smem_u32(fbuf + f * 2 * kPageBytes));
+                    wait_or_abort(&ct->f_full[f], (it / kFStages) & 1, p, &ct->abort);
+                    wait_or_abort(&ct->p_ready[x][b], ((sn + i) >> 1) & 1, p, &ct->abort);
                     if (aborted()) continue;
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)  // 16 tokens each: four of each page
-                        mma_f16_ts(od, sd + 8 * k, sw128_desc(fa + (k >> 2) * 2 * kPageBytes + 32 * (k & 3)), idesc_o, i + k > 0);
+                    for (int k = 0; k < 4; ++k)  // 16 tokens each
+                        mma_f16_ts(od, sd + 64 * b + 8 * k, fd + 2 * k, desc_hi(128), idesc_o, k > 0 ? 1 : i > 0);
                     tc_commit(&ct->o_ready[x]);
                     tc_commit(&ct->f_empty[f]);
+                    if (i + 2 < steps) scores(i + 2);
                 }
-                base += stages;
+                sn += steps;
+                base += pages;
             }
             if (lane == 0 && aborted()) {
                 // no block ends with products in flight
@@ -425,8 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
         for (long long u = u0; u < u1;) {
             const Segment s = locate(sq, c.B, G, TR, u, u1);
             const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b];
-            const int stages = (s.pe - s.p0 + 1) / 2;
-            const int steps = TWO ? stages : (stages + 1 - x) / 2, others = TWO ? stages : (stages + x) / 2;
+            const int pages = s.pe - s.p0, steps = TWO ? pages : (pages + 1 - x) / 2;
             const int row0 = s.tile * TR + (TWO ? kRows * x : 0);  // of the stream
             // queries: two neighbouring threads a row
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // both streams are done with the last
@@ -448,49 +448,36 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 
             float ref = -INFINITY, l = 0.f;
             for (int i = 0; i < steps; ++i) {
-                const int it = base + (TWO ? i : 2 * i + x), sc = it % kScales;
+                const int it = base + (TWO ? i : 2 * i + x), sc = it % kScales, b = (sn + i) & 1;
                 wait_or_abort(&ct->sc_full[sc], (it / kScales) & 1, p, &ct->abort);
-                wait_or_abort(&ct->s_ready[x], (sn + i) & 1, p, &ct->abort);
-                // the streams' softmax steps take turns (0, 1, 0, 1, ..), so that one's
-                // products run during the other's softmax and not beside the other's
-                if (x == 1 || i > 0) asm volatile("bar.sync %0, %1;" ::"r"(2 + x), "n"(kConsumers) : "memory");
+                wait_or_abort(&ct->s_ready[x][b], ((sn + i) >> 1) & 1, p, &ct->abort);
                 __syncwarp();
                 tc_fence_after();
-                float a[4][32];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) tc_ld32(ts + 32 * h, a[h]);
-                const float2 ks = *reinterpret_cast<const float2 *>(ct->ks[sc]), vs = *reinterpret_cast<const float2 *>(ct->vs[sc]);
-                const int pg = s.p0 + 2 * (it - base);
-                const bool none0 = ks.x < 0.f, none1 = ks.y < 0.f || pg + 1 >= s.pe;  // no such page
+                float a[2][32];
+                tc_ld32(ts + 64 * b, a[0]);
+                tc_ld32(ts + 64 * b + 32, a[1]);
+                const float ks = ct->ks[sc], vs = ct->vs[sc];
+                const int pg = s.p0 + it - base;
+                float fs = qs * ks;
+                if (fs == 0.f) fs = 1.17549435e-38f;  // masked scores (-inf) stay what they are
                 tc_wait_ld();
-                if (none0 || none1 || (pg + 2) * kPage > tile_sees) {
-                    const int lim0 = none0 ? 0 : sees - pg * kPage, lim1 = none1 ? 0 : sees - (pg + 1) * kPage;
+                if (ks < 0.f || (pg + 1) * kPage > tile_sees) {
+                    const int lim = ks < 0.f ? 0 : sees - pg * kPage;
 #pragma unroll
-                    for (int h = 0; h < 4; ++h)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (32 * (h & 1) + j >= (h < 2 ? lim0 : lim1)) a[h][j] = -INFINITY;
+                    for (int j = 0; j < 64; ++j)
+                        if (j >= lim) a[j >> 5][j & 31] = -INFINITY;
                 }
                 // the largest, in log2 units (a row's factor is not negative)
-                float fs[2] = {qs * ks.x, qs * ks.y};
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    if (fs[y] == 0.f) fs[y] = 1.17549435e-38f;  // masked scores (-inf) stay what they are
-                const float lv[2] = {scale_log2(vs.x), scale_log2(vs.y)};
-                float mx = -INFINITY;
+                for (int j = 0; j < 64; j += 8)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int j = 0; j < 64; j += 8)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const float *w = &a[2 * y + (j >> 5)][j & 31];
-                            m4[z] = fmaxf(m4[z], fmaxf(w[z], w[z + 4]));
-                        }
-                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    if (m > -INFINITY) mx = fmaxf(mx, fmaf(m, fs[y], lv[y]));
-                }
+                    for (int z = 0; z < 4; ++z) {
+                        const float *w = &a[j >> 5][j & 31];
+                        m4[z] = fmaxf(m4[z], fmaxf(w[z], w[z + 4]));
+                    }
+                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const float mx = m > -INFINITY ? fmaf(m, fs, scale_log2(vs)) : -INFINITY;
                 const bool move = mx > ref + kSlack;  // (ref = -inf: as soon as anything is seen)
                 if (__any_sync(0xffffffffu, move)) {
                     const float nref = move ? mx : ref;
@@ -504,52 +491,46 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 #pragma unroll 1
                         for (int h = 0; h < D / 16; ++h) {
                             float v[16];
-                            uint32_t b[16];
+                            uint32_t w[16];
                             tc_ld16(to + 16 * h, v);
                             tc_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) b[j] = __float_as_uint(v[j] * f);
-                            tc_st16(to + 16 * h, b);
+                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j] * f);
+                            tc_st16(to + 16 * h, w);
                         }
                     }
                 }
                 // 64 w vs in fp16, over the scores; w's sum from the unrounded values
+                const float pv = fmaxf(vs, 0x1p-64f) * kGain, add = __log2f(pv) - (ref == -INFINITY ? 0.f : ref);
+                const uint64_t f2 = pack2(fs, fs), a2 = pack2(add, add);
+                uint64_t l2[2] = {0, 0};
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float pv = fmaxf(y ? vs.y : vs.x, 0x1p-64f) * kGain;
-                    const float add = __log2f(pv) - (ref == -INFINITY ? 0.f : ref);
-                    const uint64_t f2 = pack2(fs[y], fs[y]), add2v = pack2(add, add);
-                    uint64_t l2[2] = {0, 0};
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int h = 2 * y + hh;
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float e0, e1;
-                            unpack2(fma2(pack2(a[h][2 * j], a[h][2 * j + 1]), f2, add2v), e0, e1);
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
-                            l2[j & 1] = add2(l2[j & 1], pack2(e0, e1));
-                            w[j] = cvt_f16x2(e0, e1);
-                        }
-                        tc_st16(ts + 16 * h, w);
+                    for (int j = 0; j < 16; ++j) {
+                        float e0, e1;
+                        unpack2(fma2(pack2(a[h][2 * j], a[h][2 * j + 1]), f2, a2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        l2[j & 1] = add2(l2[j & 1], pack2(e0, e1));
+                        w[j] = cvt_f16x2(e0, e1);
                     }
-                    float e0, e1;
-                    unpack2(add2(l2[0], l2[1]), e0, e1);
-                    l += (e0 + e1) * (1.f / pv);
+                    tc_st16(ts + 64 * b + 16 * h, w);
                 }
-                if (i + x < others) asm volatile("bar.arrive %0, %1;" ::"r"(3 - x), "n"(kConsumers) : "memory");
+                float e0, e1;
+                unpack2(add2(l2[0], l2[1]), e0, e1);
+                l += (e0 + e1) * (1.f / pv);
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(&ct->p_ready[x]);
+                mbar_arrive(&ct->p_ready[x][b]);
             }
             sn += steps;
-            on[0] += TWO ? stages : (stages + 1) / 2;
-            on[1] += TWO ? stages : stages / 2;
+            on[0] += TWO ? pages : (pages + 1) / 2;
+            on[1] += TWO ? pages : pages / 2;
 
             // ---- the result: o / 64 in tensor memory, references and sums
-            const bool have0 = stages > 0, have1 = !TWO && stages > 1;
+            const bool have0 = pages > 0, have1 = !TWO && pages > 1;
             const int x0 = TWO ? x : 0;
             float f0 = 1.f, f1 = 0.f, msum = ref, lsum = l;
             if (!TWO) {  // the streams' together
@@ -605,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             }
             tc_fence_before();
             if (!s.whole()) join_tile<D, kConsumers>(p, s, U, blocks, TR, rows, q0, G, kGain, &ct->last);
-            base += stages;
+            base += pages;
             u += s.p1 - s.p0;
         }
     }
@@ -619,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 template <int D, bool TWO>
 cudaError_t launch_one(const AttendParams &p, int grid, cudaStream_t st)
 {
-    // k, v, v in fp16 (twice as many bytes, two buffers), query digits
-    constexpr int smem = 1024 + 2 * kPage * D * (kKStages + kVStages + 4) + (TWO ? 2 : 1) * 2 * kRows * D +
+    // pages of k, of v, of v in fp16 (twice as many bytes), query digits
+    constexpr int smem = 1024 + kPage * D * (kKStages + kVStages + 2 * kFStages) + (TWO ? 2 : 1) * 2 * kRows * D +
                          static_cast<int>(sizeof(Control) + sizeof(Seqs));
     static_assert(smem <= 227 * 1024, "shared memory of a block");
     auto *fn = moe_kv_attend_tc_kernel<D, TWO>;
