@@ -4,34 +4,33 @@
 //   o[i, h] = sum_t w_t v[t] / sum_t w_t,   w_t = 2^(s_t - ref),
 //   s_t = log2(e) scale q.k_t
 //
-// Both products run on the tensor cores (tcgen05.mma), their accumulators in
-// tensor memory:
+// A tile is 128 query rows, a step 128 tokens (two pages).  Both products run on
+// the tensor cores (tcgen05.mma), their accumulators in tensor memory:
 //
-//  * S[128 rows x 64 tokens of a page] = Q K^T, kind::f8f6f4 on the cache's E4M3 codes as TMA
-//    brings them: q enters as two E4M3 digits, hi + lo, after a power-of-two
-//    prescale of the row (largest magnitude into [128, 256)): 8 significant bits
-//    are two digits of 4, so the sum is exact down to 2^-10 of the row's
-//    largest.  Two digits at twice the 16-bit rate cost what 16-bit operands would.
-//  * O[128 rows x head dim] += P V, kind::f16: the weights 64 w vs (vs: the page's v
-//    scale over the largest that the reference allows for) are rounded to fp16 and
-//    written to tensor memory over the scores they come from.  v's codes become
-//    fp16 (exact) in shared memory, once for all rows of the block; digits for the
-//    weights instead would cost the softmax threads, which bound the kernel, three
-//    more instructions a weight.
+//  * S = Q K^T, kind::f8f6f4 on the cache's E4M3 codes as TMA brings them: q enters
+//    as two E4M3 digits, hi + lo, after a power-of-two prescale of the row (largest
+//    magnitude into [128, 256)): 8 significant bits are two digits of 4, so the
+//    sum is exact down to 2^-10 of the row's largest.  Two digits at twice the
+//    16-bit rate cost what 16-bit operands would.
+//  * O += P V, kind::f16: the weights 64 w vs (vs: the page's v scale over the largest
+//    that the reference allows for) are rounded to fp16 and written to tensor
+//    memory.  v's codes become fp16 (exact) in shared memory; two digits for the
+//    weights instead would cost the softmax three more instructions a weight.
 //
 // The reference is the running maximum of s + ceil(log2(vs)), moved only when a
 // step exceeds it by more than 8 (fp16 holds 64 * 2^8), so the accumulators in
 // tensor memory are rescaled rarely.
 //
-// A block runs two streams, each with a warpgroup for the softmax (a thread a
-// row), a thread that issues its MMAs, and in tensor memory its own O and two S / P
-// buffers: the scores of the next page are computed while the softmax works on
-// this one's, so that it never waits for the chain from its weights over P V to
-// the next scores (with one buffer of 128 tokens that chain, mostly latencies, took
-// longer than the softmax: 580 against ~XXX us for 2048 x 16384, 32 heads).
-// With TWO, the streams are two row tiles that share the pages; otherwise they
-// are the even and the odd pages of one row tile, joined at the end.  One warp
-// brings pages; a warpgroup converts v.
+// A group of eight MMAs takes 800 cycles from issue to its barrier, 512 of them at
+// work, and a softmax step about 1700: so steps overlap.  Two warpgroups take the
+// steps in turn (a thread a row), each with its own S and P in tensor memory; the
+// scores of a warpgroup's next step are computed once it has read this one's,
+// and P V during the following softmax.  Only the reference goes from step to step, as
+// soon as a step's maxima are known.  One warp brings pages, one thread issues
+// the products for S and one those for O, a warpgroup converts v.  With two row
+// tiles a block sharing k and v, tensor memory leaves no room for this (S and P in one
+// place): the softmax then waits for the chain from its weights over P V to the next
+// scores, 580 us for 2048 x 16384 tokens and 32 heads.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -49,27 +48,31 @@ namespace {
 
 #include "moe_attend.cuh"
 
-constexpr int kRows = 128;       // rows of a stream: tensor-memory lanes, softmax threads
+constexpr int kRows = 128;       // rows of a tile: tensor-memory lanes, threads of a softmax warpgroup
 constexpr int kConsumers = 2 * kRows;
 constexpr int kThreads = kConsumers + 256;  // and a warpgroup that converts v, one with the producer and the issuers
 // Registers a thread of the two kinds keeps: 256 * 200 + 256 * 56 = 65536, what the
 // block is launched with (512 threads of 128).
 constexpr int kConsumerRegs = 200, kOtherRegs = 56;
+constexpr int kKeys = 2 * kPage; // tokens of a step
 constexpr float kGain = 64.f;    // of the weights
 constexpr float kSlack = 8.f;    // how far a step may exceed the reference (64 * 2^8 is inside fp16)
-constexpr int kTmemCols = 512;   // stream s: S / P buffer b at 256 s + 64 b, O at 256 s + 128
-constexpr int kKStages = 6, kVStages = 4, kFStages = 4;  // pages of k, of v, of v in fp16
-constexpr int kScales = 16;      // pages whose scales are kept: more than a softmax lags behind the producer (10)
+// Tensor memory: warpgroup b's S at 128 b, its P at 256 + 64 b, O at 384.
+constexpr int kTmemCols = 512, kTmemP = 256, kTmemO = 384;
+constexpr int kKStages = 4, kVStages = 3, kFStages = 2;  // steps of k, of v, of v in fp16
+constexpr int kScales = 8;       // steps whose scales are kept: more than a softmax lags behind the producer
 
 struct Control {
     uint64_t k_full[kKStages], k_empty[kKStages];   // codes of k
     uint64_t v_full[kVStages], v_empty[kVStages];   // codes of v
     uint64_t f_full[kFStages], f_empty[kFStages];   // v in fp16
     uint64_t sc_full[kScales];
-    uint64_t q_ready, s_ready[2][2], p_ready[2][2], o_ready[2], drained[2];  // [stream][buffer]
-    float ks[kScales], vs[kScales];        // a page's scales; ks < 0: no such page
-    float qs[2][kRows];                    // each row's factor from digits to scores (log2 units)
-    float m[2][kRows], l[2][kRows];        // the streams' references and sums, for joining them
+    uint64_t q_ready, drained[2];
+    uint64_t s_ready[2], s_read[2], ref_ready[2], p_ready[2], o_ready[2];  // of the warpgroups' steps
+    float ks[kScales][2], vs[kScales][2];  // scales of a step's pages; ks < 0: no such page
+    float qs[kRows];                       // each row's factor from digits to scores (log2 units)
+    float ref[2][kRows];                   // the reference after a warpgroup's last step
+    float l[2][kRows], lref[2][kRows];     // the warpgroups' sums at a tile's end and what they refer to
     uint32_t tmem;
     int abort, last;
 };
@@ -151,7 +154,7 @@ __device__ __forceinline__ int granule(int row, int gr)
     return row * D + ((D == 128 ? gr ^ (row & 7) : gr ^ ((row >> 1) & 3)) << 4);
 }
 
-// Half a query row (thread pairs share a row) as two digits into the tile at dst
+// Half a query row (two neighbouring threads share a row) as two digits into the tile at dst
 // (hi; lo follows kRows * D bytes on); returns the row's factor.
 template <int D>
 __device__ __forceinline__ float put_query(uint8_t *dst, int row, int half, const uint16_t *src, bool in, float scale)
@@ -214,17 +217,16 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
     return d;
 }
 
-template <int D, bool TWO>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __grid_constant__ AttendParams p)
 {
-    constexpr int TR = TWO ? 2 * kRows : kRows;  // query rows of a tile
+    constexpr int TR = kRows;
     constexpr int kPageBytes = kPage * D;
-    constexpr int kQ = 2 * kRows * D;            // a stream's query digits
+    constexpr int kStep = 2 * kPageBytes;  // a step's codes of k, or of v
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *kbuf = smem, *vbuf = kbuf + kKStages * kPageBytes, *fbuf = vbuf + kVStages * kPageBytes;
-    uint8_t *qbuf = fbuf + kFStages * 2 * kPageBytes;
-    Control *ct = reinterpret_cast<Control *>(qbuf + (TWO ? 2 : 1) * kQ);
+    uint8_t *kbuf = smem, *vbuf = kbuf + kKStages * kStep, *fbuf = vbuf + kVStages * kStep, *qbuf = fbuf + kFStages * 2 * kStep;
+    Control *ct = reinterpret_cast<Control *>(qbuf + 2 * kRows * D);
     Seqs &sq = *reinterpret_cast<Seqs *>(reinterpret_cast<uint8_t *>(ct) + sizeof(Control));
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const KvParams &c = p.c;
@@ -233,28 +235,27 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 
     if (tid == 0) {
         ct->abort = 0;
-        const int streams = TWO ? 2 : 1;  // that use a page
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(&ct->k_full[i], 1);
-            mbar_init(&ct->k_empty[i], streams);
+            mbar_init(&ct->k_empty[i], 1);
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&ct->v_full[i], 1);
             mbar_init(&ct->v_empty[i], 128);
         }
-        for (int i = 0; i < kScales; ++i) mbar_init(&ct->sc_full[i], 1);
-        mbar_init(&ct->q_ready, kConsumers);
         for (int i = 0; i < kFStages; ++i) {
             mbar_init(&ct->f_full[i], 128);
-            mbar_init(&ct->f_empty[i], streams);
+            mbar_init(&ct->f_empty[i], 1);
         }
-        for (int s = 0; s < 2; ++s) {
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&ct->s_ready[s][b], 1);
-                mbar_init(&ct->p_ready[s][b], kRows);
-            }
-            mbar_init(&ct->o_ready[s], 1);
-            mbar_init(&ct->drained[s], 1);
+        for (int i = 0; i < kScales; ++i) mbar_init(&ct->sc_full[i], 1);
+        mbar_init(&ct->q_ready, kConsumers);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ct->drained[b], 1);
+            mbar_init(&ct->s_ready[b], 1);
+            mbar_init(&ct->s_read[b], kRows);
+            mbar_init(&ct->ref_ready[b], kRows);
+            mbar_init(&ct->p_ready[b], kRows);
+            mbar_init(&ct->o_ready[b], 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -280,16 +281,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             int it = 0;
             for (long long u = u0; u < u1;) {
                 const Segment s = locate(sq, c.B, G, TR, u, u1);
-                const int end = it + s.pe - s.p0;
+                const int end = it + (s.pe - s.p0 + 1) / 2;
                 for (; it < end; ++it) {
                     const int vs = it % kVStages, f = it % kFStages;
                     wait_or_abort(&ct->v_full[vs], (it / kVStages) & 1, p, &ct->abort);
                     if (it >= kFStages) wait_or_abort(&ct->f_empty[f], (it / kFStages - 1) & 1, p, &ct->abort);
                     __syncwarp();
-                    const uint8_t *src = vbuf + vs * kPageBytes;
-                    uint8_t *dst = fbuf + f * 2 * kPageBytes;
+                    const uint8_t *src = vbuf + vs * kStep;
+                    uint8_t *dst = fbuf + f * 2 * kStep;
 #pragma unroll 4
-                    for (int i = t; i < kPageBytes / 16; i += 128) {  // 16 codes: granule i % 4 of row i / 4
+                    for (int i = t; i < kStep / 16; i += 128) {  // 16 codes: granule i % 4 of row i / 4
                         const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
                         uint32_t h[8];
 #pragma unroll
@@ -308,34 +309,46 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 u += s.p1 - s.p0;
             }
         } else if (wid == kProducer) {
-            // ---- producer
+            // ---- producer: two pages a step; an odd last page comes twice (the second
+            // copy is behind every row's mask)
             int it = 0;
-            const uint64_t pol = TWO ? policy_evict_last() : policy_evict_first();  // other tiles read the page too
+            const uint64_t pol = policy_evict_last();  // other tiles read the page too
             for (long long u = u0; u < u1;) {
                 const Segment s = locate(sq, c.B, G, TR, u, u1);
                 for (int pb = s.p0; pb < s.pe; pb += 32) {
                     const PageInfo pi = load_pages(c, s, pb);
                     const int m = min(32, s.pe - pb);
-                    for (int i = 0; i < m; ++i, ++it) {
+                    for (int i = 0; i < m; i += 2, ++it) {
                         const int ks = it % kKStages, vs = it % kVStages, sc = it % kScales;
-                        const int pid = __shfl_sync(0xffffffffu, pi.id, i);
-                        const float pks = __shfl_sync(0xffffffffu, pi.ks, i), pvs = __shfl_sync(0xffffffffu, pi.vs, i);
-                        if (lane == 0) {
+                        int ph[2];
+                        float pks[2], pvs[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int src = min(i + x, m - 1);
                             // a page out of range is masked; page 0 stands in for its codes
-                            const int ph = max(pid, 0) * c.kv_heads + s.h;
+                            ph[x] = max(__shfl_sync(0xffffffffu, pi.id, src), 0) * c.kv_heads + s.h;
+                            pks[x] = __shfl_sync(0xffffffffu, pi.ks, src);
+                            pvs[x] = __shfl_sync(0xffffffffu, pi.vs, src);
+                        }
+                        if (lane == 0) {
                             if (it >= kKStages) wait_or_abort(&ct->k_empty[ks], (it / kKStages - 1) & 1, p, &ct->abort);
                             if (!aborted()) {
-                                ct->ks[sc] = pks;
-                                ct->vs[sc] = pvs;
+                                mbar_expect_tx(&ct->k_full[ks], kStep);
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    ct->ks[sc][x] = pks[x];
+                                    ct->vs[sc][x] = pvs[x];
+                                    tma2d(kbuf + ks * kStep + x * kPageBytes, &c.tm_k, 0, ph[x] * kPage, &ct->k_full[ks], pol);
+                                }
                                 mbar_arrive(&ct->sc_full[sc]);
-                                mbar_expect_tx(&ct->k_full[ks], kPageBytes);
-                                tma2d(kbuf + ks * kPageBytes, &c.tm_k, 0, ph * kPage, &ct->k_full[ks], pol);
                             }
                             if (it >= kVStages) wait_or_abort(&ct->v_empty[vs], (it / kVStages - 1) & 1, p, &ct->abort);
                             if (!aborted()) {
-                                mbar_expect_tx(&ct->v_full[vs], kPageBytes);
-                                bulk_g2s(vbuf + vs * kPageBytes, c.v + static_cast<size_t>(ph) * kPageBytes, kPageBytes,
-                                         &ct->v_full[vs], pol);
+                                mbar_expect_tx(&ct->v_full[vs], kStep);
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    bulk_g2s(vbuf + vs * kStep + x * kPageBytes, c.v + static_cast<size_t>(ph[x]) * kPageBytes,
+                                             kPageBytes, &ct->v_full[vs], pol);
                             }
                         }
                         __syncwarp();
@@ -355,87 +368,78 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     }
             }
         } else if (wid == kIssuer || wid == kIssuer + 1) {
-            // ---- MMA issue: a thread for each stream (its warp finds the segments), so
-            // that a stream waits only for its own
-            const int x = wid - kIssuer;
-            const uint32_t idesc_s = mma_idesc(kPage), idesc_o = mma_idesc(D);
-            const uint32_t sd = tmem + 256 * x, od = sd + 128;
-            int base = 0, nseg = 0;  // pages before the segment; segments so far
-            uint32_t sn = 0;         // steps so far
+            // ---- MMA issue, one thread for S and one for O (their warps find the
+            // segments).  A block that gave up goes on without waiting, on whatever is there.
+            const bool scores = wid == kIssuer;
+            const uint32_t qd = desc_lo(smem_u32(qbuf)), kd = desc_lo(smem_u32(kbuf)), fd = desc_lo(smem_u32(fbuf));
+            int slot = 0, nseg = 0;      // buffer of the next step; segments so far
+            uint32_t phase = 0, n = 0;   // of that buffer; steps so far
             for (long long u = u0; u < u1; ++nseg) {
                 const Segment s = locate(sq, c.B, G, TR, u, u1);
-                const int pages = s.pe - s.p0, steps = TWO ? pages : (pages + 1 - x) / 2;
+                const int steps = (s.pe - s.p0 + 1) / 2;
                 u += s.p1 - s.p0;
                 __syncwarp();
                 if (lane != 0) continue;
-                wait_or_abort(&ct->q_ready, nseg & 1, p, &ct->abort);
-                tc_fence_after();
-                const uint32_t qd = desc_lo(smem_u32(qbuf) + (TWO ? x * kQ : 0));
-                auto scores = [&](int i) {  // of step i, into buffer (sn + i) & 1
-                    const int it = base + (TWO ? i : 2 * i + x), ks = it % kKStages, b = (sn + i) & 1;
-                    const uint32_t kd = desc_lo(smem_u32(kbuf + ks * kPageBytes)), d = sd + 64 * b;
-                    wait_or_abort(&ct->k_full[ks], (it / kKStages) & 1, p, &ct->abort);
-                    // they take the place of the weights of the step before the last
-                    if (i > 1) wait_or_abort(&ct->o_ready[x], (sn + i) & 1, p, &ct->abort);
-                    if (aborted()) return;
-                    tc_fence_after();
-                    mma_f8<false>(d, qd, kd, desc_hi(D), idesc_s);
+                if (scores) {
+                    wait_or_abort(&ct->q_ready, nseg & 1, p, &ct->abort);
+                    for (int i = 0; i < steps; ++i, ++n) {
+                        const uint32_t b = n & 1, d = tmem + 128 * b, k = kd + slot * (kStep / 16);
+                        wait_or_abort(&ct->k_full[slot], phase, p, &ct->abort);
+                        if (n >= 2) wait_or_abort(&ct->s_read[b], (n / 2 - 1) & 1, p, &ct->abort);
+                        tc_fence_after();
+                        mma_f8<false>(d, qd, k, desc_hi(D), mma_idesc(kKeys));
 #pragma unroll
-                    for (int k = 1; k < D / 32; ++k) mma_f8<true>(d, qd + 2 * k, kd + 2 * k, desc_hi(D), idesc_s);
+                        for (int j = 1; j < D / 32; ++j) mma_f8<true>(d, qd + 2 * j, k + 2 * j, desc_hi(D), mma_idesc(kKeys));
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        mma_f8<true>(d, qd + kRows * D / 16 + 2 * k, kd + 2 * k, desc_hi(D), idesc_s);
-                    tc_commit(&ct->s_ready[x][b]);
-                    tc_commit(&ct->k_empty[ks]);
-                };
-                if (steps > 0) scores(0);
-                if (steps > 1) scores(1);
-                for (int i = 0; i < steps; ++i) {
-                    const int it = base + (TWO ? i : 2 * i + x), f = it % kFStages, b = (sn + i) & 1;
-                    const uint32_t fd = desc_lo(smem_u32(fbuf + f * 2 * kPageBytes));
-                    wait_or_abort(&ct->f_full[f], (it / kFStages) & 1, p, &ct->abort);
-                    wait_or_abort(&ct->p_ready[x][b], ((sn + i) >> 1) & 1, p, &ct->abort);
-                    if (aborted()) continue;
-                    tc_fence_after();
+                        for (int j = 0; j < D / 32; ++j)
+                            mma_f8<true>(d, qd + kRows * D / 16 + 2 * j, k + 2 * j, desc_hi(D), mma_idesc(kKeys));
+                        tc_commit(&ct->s_ready[b]);
+                        tc_commit(&ct->k_empty[slot]);
+                        if (++slot == kKStages) slot = 0, phase ^= 1;
+                    }
+                } else {
+                    for (int i = 0; i < steps; ++i, ++n) {
+                        const uint32_t b = n & 1, a = tmem + kTmemP + 64 * b, f = fd + slot * (2 * kStep / 16);
+                        wait_or_abort(&ct->f_full[slot], phase, p, &ct->abort);
+                        wait_or_abort(&ct->p_ready[b], (n / 2) & 1, p, &ct->abort);
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 16 tokens each
-                        mma_f16_ts(od, sd + 64 * b + 8 * k, fd + 2 * k, desc_hi(128), idesc_o, k > 0 ? 1 : i > 0);
-                    tc_commit(&ct->o_ready[x]);
-                    tc_commit(&ct->f_empty[f]);
-                    if (i + 2 < steps) scores(i + 2);
+                        for (int j = 0; j < 8; ++j)  // 16 tokens each: four of each page
+                            mma_f16_ts(tmem + kTmemO, a + 8 * j, f + (j >> 2) * (2 * kPageBytes / 16) + 2 * (j & 3), desc_hi(128),
+                                       mma_idesc(D), j > 0 ? 1 : i > 0);
+                        tc_commit(&ct->o_ready[b]);
+                        tc_commit(&ct->f_empty[slot]);
+                        if (++slot == kFStages) slot = 0, phase ^= 1;
+                    }
                 }
-                sn += steps;
-                base += pages;
             }
             if (lane == 0 && aborted()) {
                 // no block ends with products in flight
-                tc_commit(&ct->drained[x]);
+                tc_commit(&ct->drained[scores]);
                 const uint64_t t0 = gtimer();
-                while (!mbar_test(&ct->drained[x], 0) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
+                while (!mbar_test(&ct->drained[scores], 0) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
                 }
             }
         }
     } else {
-        // ---- softmax: stream x, a thread a row
+        // ---- softmax: warpgroup w takes the steps n with n % 2 = w, a thread a row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
-        const int x = wid >> 2, row = tid & (kRows - 1);
+        const uint32_t w = wid >> 2;
+        const int row = tid & (kRows - 1);
         const uint32_t lanes = static_cast<uint32_t>(wid & 3) << 21;  // this warp's tensor-memory lanes
-        const uint32_t ts = tmem + 256 * x + lanes, to = ts + 128;
-        int base = 0;
-        uint32_t sn = 0, on[2] = {0, 0};  // this stream's steps so far; both streams'
+        const uint32_t ts = tmem + lanes + 128 * w, tp = tmem + lanes + kTmemP + 64 * w, to = tmem + lanes + kTmemO;
+        uint32_t n0 = 0;  // steps before the segment
         for (long long u = u0; u < u1;) {
             const Segment s = locate(sq, c.B, G, TR, u, u1);
-            const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b];
-            const int pages = s.pe - s.p0, steps = TWO ? pages : (pages + 1 - x) / 2;
-            const int row0 = s.tile * TR + (TWO ? kRows * x : 0);  // of the stream
-            // queries: two neighbouring threads a row
-            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // both streams are done with the last
-            for (int part = 0; part < (TWO ? 2 : 1); ++part) {
-                const int qr = 64 * (TWO ? part : x) + (row >> 1), r = row0 + qr;
-                const float f = put_query<D>(qbuf + (TWO ? x * kQ : 0), qr, row & 1,
+            const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b], row0 = s.tile * TR;
+            const int steps = (s.pe - s.p0 + 1) / 2;
+            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last segment is over
+            {
+                const int qr = tid >> 1, r = row0 + qr;
+                const float f = put_query<D>(qbuf, qr, tid & 1,
                                              p.q + static_cast<long long>(q0 + r / G) * p.q_stride + (s.h * G + r % G) * D,
                                              r < rows, p.scale_log2);
-                if ((row & 1) == 0) ct->qs[TWO ? x : 0][qr] = f;
+                if ((tid & 1) == 0) ct->qs[qr] = f;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
@@ -443,135 +447,148 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             const int r = row0 + row;
             const int sees = r < rows ? row_sees(len, n, G, r) : 0;
-            const float qs = sees > 0 ? ct->qs[TWO ? x : 0][row] : 0.f;
-            const int tile_sees = row_sees(len, n, G, row0);  // the least of the stream's rows
+            const float qs = sees > 0 ? ct->qs[row] : 0.f;
+            const int tile_sees = row_sees(len, n, G, row0);  // the least of the tile's rows
 
-            float ref = -INFINITY, l = 0.f;
-            for (int i = 0; i < steps; ++i) {
-                const int it = base + (TWO ? i : 2 * i + x), sc = it % kScales, b = (sn + i) & 1;
-                wait_or_abort(&ct->sc_full[sc], (it / kScales) & 1, p, &ct->abort);
-                wait_or_abort(&ct->s_ready[x][b], ((sn + i) >> 1) & 1, p, &ct->abort);
+            float l = 0.f, lref = -INFINITY;  // this warpgroup's sum and what it refers to
+            for (int i = (n0 & 1) == w ? 0 : 1; i < steps; i += 2) {
+                const uint32_t k = n0 + i, ph = (k >> 1) & 1, sc = k % kScales;  // step, its barriers' phase
+                wait_or_abort(&ct->sc_full[sc], (k / kScales) & 1, p, &ct->abort);
+                wait_or_abort(&ct->s_ready[w], ph, p, &ct->abort);
                 __syncwarp();
                 tc_fence_after();
-                float a[2][32];
-                tc_ld32(ts + 64 * b, a[0]);
-                tc_ld32(ts + 64 * b + 32, a[1]);
-                const float ks = ct->ks[sc], vs = ct->vs[sc];
-                const int pg = s.p0 + it - base;
-                float fs = qs * ks;
-                if (fs == 0.f) fs = 1.17549435e-38f;  // masked scores (-inf) stay what they are
-                tc_wait_ld();
-                if (ks < 0.f || (pg + 1) * kPage > tile_sees) {
-                    const int lim = ks < 0.f ? 0 : sees - pg * kPage;
+                float a[4][32];
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (j >= lim) a[j >> 5][j & 31] = -INFINITY;
+                for (int h = 0; h < 4; ++h) tc_ld32(ts + 32 * h, a[h]);
+                const float2 ks = *reinterpret_cast<const float2 *>(ct->ks[sc]), vs = *reinterpret_cast<const float2 *>(ct->vs[sc]);
+                const int pg = s.p0 + 2 * i;
+                const bool none0 = ks.x < 0.f, none1 = ks.y < 0.f || pg + 1 >= s.pe;  // no such page
+                tc_wait_ld();
+                tc_fence_before();
+                mbar_arrive(&ct->s_read[w]);
+                if (none0 || none1 || (pg + 2) * kPage > tile_sees) {
+                    const int lim0 = none0 ? 0 : sees - pg * kPage, lim1 = none1 ? 0 : sees - (pg + 1) * kPage;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * (h & 1) + j >= (h < 2 ? lim0 : lim1)) a[h][j] = -INFINITY;
                 }
                 // the largest, in log2 units (a row's factor is not negative)
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float fs[2] = {qs * ks.x, qs * ks.y};
+                float mx = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 64; j += 8)
+                for (int y = 0; y < 2; ++y) {
+                    if (fs[y] == 0.f) fs[y] = 1.17549435e-38f;  // masked scores (-inf) stay what they are
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float *w = &a[j >> 5][j & 31];
-                        m4[z] = fmaxf(m4[z], fmaxf(w[z], w[z + 4]));
-                    }
-                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                const float mx = m > -INFINITY ? fmaf(m, fs, scale_log2(vs)) : -INFINITY;
-                const bool move = mx > ref + kSlack;  // (ref = -inf: as soon as anything is seen)
-                if (__any_sync(0xffffffffu, move)) {
-                    const float nref = move ? mx : ref;
-                    const float f = move ? ex2(ref - nref) : 1.f;
-                    l *= f;
-                    ref = nref;
-                    if (i > 0) {
-                        wait_or_abort(&ct->o_ready[x], (sn + i - 1) & 1, p, &ct->abort);
-                        __syncwarp();
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int h = 0; h < D / 16; ++h) {
-                            float v[16];
-                            uint32_t w[16];
-                            tc_ld16(to + 16 * h, v);
-                            tc_wait_ld();
+                    for (int j = 0; j < 64; j += 8)
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j] * f);
-                            tc_st16(to + 16 * h, w);
+                        for (int z = 0; z < 4; ++z) {
+                            const float *v = &a[2 * y + (j >> 5)][j & 31];
+                            m4[z] = fmaxf(m4[z], fmaxf(v[z], v[z + 4]));
                         }
+                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    if (m > -INFINITY) mx = fmaxf(mx, fmaf(m, fs[y], scale_log2(y ? vs.y : vs.x)));
+                }
+                // the reference after the step before, from the other warpgroup
+                float ref = -INFINITY;
+                if (i > 0) {
+                    wait_or_abort(&ct->ref_ready[w ^ 1], ((k - 1) >> 1) & 1, p, &ct->abort);
+                    ref = ct->ref[w ^ 1][row];
+                }
+                const bool move = mx > ref + kSlack;  // (ref = -inf: as soon as anything is seen)
+                const float old = ref;
+                if (move) ref = mx;
+                ct->ref[w][row] = ref;
+                mbar_arrive(&ct->ref_ready[w]);
+                if (__any_sync(0xffffffffu, move) && i > 0) {
+                    // the accumulators follow, between the last step's product and this one's
+                    wait_or_abort(&ct->o_ready[w ^ 1], ((k - 1) >> 1) & 1, p, &ct->abort);
+                    __syncwarp();
+                    tc_fence_after();
+                    const float f = move ? ex2(old - ref) : 1.f;
+#pragma unroll 1
+                    for (int h = 0; h < D / 16; ++h) {
+                        float v[16];
+                        uint32_t x[16];
+                        tc_ld16(to + 16 * h, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(v[j] * f);
+                        tc_st16(to + 16 * h, x);
                     }
                 }
-                // 64 w vs in fp16, over the scores; w's sum from the unrounded values
-                const float pv = fmaxf(vs, 0x1p-64f) * kGain, add = __log2f(pv) - (ref == -INFINITY ? 0.f : ref);
-                const uint64_t f2 = pack2(fs, fs), a2 = pack2(add, add);
-                uint64_t l2[2] = {0, 0};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float e0, e1;
-                        unpack2(fma2(pack2(a[h][2 * j], a[h][2 * j + 1]), f2, a2), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        l2[j & 1] = add2(l2[j & 1], pack2(e0, e1));
-                        w[j] = cvt_f16x2(e0, e1);
-                    }
-                    tc_st16(ts + 64 * b + 16 * h, w);
+                const float base = ref == -INFINITY ? 0.f : ref;
+                if (lref != ref) l *= ex2(lref - base);  // (lref = -inf: 0, as l is)
+                lref = ref;
+                if (i > 1) {  // the last weights in this warpgroup's place have been used
+                    wait_or_abort(&ct->o_ready[w], ph ^ 1, p, &ct->abort);
+                    __syncwarp();
+                    tc_fence_after();
                 }
-                float e0, e1;
-                unpack2(add2(l2[0], l2[1]), e0, e1);
-                l += (e0 + e1) * (1.f / pv);
+                // 64 w vs in fp16; w's sum from the unrounded values
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float pv = fmaxf(y ? vs.y : vs.x, 0x1p-64f) * kGain, add = __log2f(pv) - base;
+                    const uint64_t f2 = pack2(fs[y], fs[y]), a2 = pack2(add, add);
+                    uint64_t l2[2] = {0, 0};
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int h = 2 * y + hh;
+                        uint32_t x[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float e0, e1;
+                            unpack2(fma2(pack2(a[h][2 * j], a[h][2 * j + 1]), f2, a2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            l2[j & 1] = add2(l2[j & 1], pack2(e0, e1));
+                            x[j] = cvt_f16x2(e0, e1);
+                        }
+                        tc_st16(tp + 16 * h, x);
+                    }
+                    float e0, e1;
+                    unpack2(add2(l2[0], l2[1]), e0, e1);
+                    l += (e0 + e1) * (1.f / pv);
+                }
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(&ct->p_ready[x][b]);
+                mbar_arrive(&ct->p_ready[w]);
             }
-            sn += steps;
-            on[0] += TWO ? pages : (pages + 1) / 2;
-            on[1] += TWO ? pages : pages / 2;
 
-            // ---- the result: o / 64 in tensor memory, references and sums
-            const bool have0 = pages > 0, have1 = !TWO && pages > 1;
-            const int x0 = TWO ? x : 0;
-            float f0 = 1.f, f1 = 0.f, msum = ref, lsum = l;
-            if (!TWO) {  // the streams' together
-                ct->m[x][row] = ref;
-                ct->l[x][row] = l;
-                asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-                const float m0 = ct->m[0][row], m1 = ct->m[1][row];
-                msum = fmaxf(m0, m1);
-                const float mref = msum == -INFINITY ? 0.f : msum;
-                f0 = ex2(m0 - mref);
-                f1 = ex2(m1 - mref);
-                lsum = ct->l[0][row] * f0 + ct->l[1][row] * f1;
+            // ---- the result: o / 64 in tensor memory, the last reference, the sums
+            ct->l[w][row] = l;
+            ct->lref[w][row] = lref;
+            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+            n0 += steps;
+            float ref = -INFINITY, lsum = 0.f;
+            if (steps > 0) {
+                const uint32_t last = n0 - 1;
+                ref = ct->ref[last & 1][row];
+                const float base = ref == -INFINITY ? 0.f : ref;
+                lsum = ct->l[0][row] * ex2(ct->lref[0][row] - base) + ct->l[1][row] * ex2(ct->lref[1][row] - base);
+                wait_or_abort(&ct->o_ready[last & 1], (last >> 1) & 1, p, &ct->abort);  // (products end in order)
+                __syncwarp();
+                tc_fence_after();
             }
-            if (have0) wait_or_abort(&ct->o_ready[x0], (on[x0] - 1) & 1, p, &ct->abort);
-            if (have1) wait_or_abort(&ct->o_ready[1], (on[1] - 1) & 1, p, &ct->abort);
-            __syncwarp();
-            tc_fence_after();
             float *part = part_slot(p, blockIdx.x, s.p0 == 0);
-            const int rr = TWO ? kRows * x + row : row;
-            if (!s.whole() && (TWO || x == 0)) {
-                part[rr] = msum;
-                part[TR + rr] = lsum;
+            if (!s.whole() && w == 0) {
+                part[row] = ref;
+                part[TR + row] = lsum;
             }
             const float inv = inv_sum(kGain, lsum);
             uint16_t *orow = out_row(p, q0, s.h, G, min(r, rows - 1));
-            constexpr int kCols = TWO ? D : D / 2;  // of this thread
-            const int col0 = TWO ? 0 : kCols * x;
+            // each warpgroup has half the head dims
 #pragma unroll 2
-            for (int col = col0; col < col0 + kCols; col += 16) {
-                float v[16], w[16];
+            for (int col = D / 2 * w; col < D / 2 * (w + 1); col += 16) {
+                float v[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = w[j] = 0.f;
-                if (have0) tc_ld16(tmem + lanes + 256 * x0 + 128 + col, v);
-                if (have1) tc_ld16(tmem + lanes + 256 + 128 + col, w);
+                for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                if (steps > 0) tc_ld16(to + col, v);
                 tc_wait_ld();
-                if (!TWO) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = v[j] * f0 + w[j] * f1;
-                }
                 if (!s.whole()) {
-                    float4 *o = reinterpret_cast<float4 *>(part + 2 * TR + rr * D + col);
+                    float4 *o = reinterpret_cast<float4 *>(part + 2 * TR + row * D + col);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else if (r < rows) {
@@ -586,7 +603,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             }
             tc_fence_before();
             if (!s.whole()) join_tile<D, kConsumers>(p, s, U, blocks, TR, rows, q0, G, kGain, &ct->last);
-            base += pages;
             u += s.p1 - s.p0;
         }
     }
@@ -597,14 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     if (wid == kIssuer) tc_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool TWO>
-cudaError_t launch_one(const AttendParams &p, int grid, cudaStream_t st)
+template <int D>
+cudaError_t launch_d(const AttendParams &p, int grid, cudaStream_t st)
 {
-    // pages of k, of v, of v in fp16 (twice as many bytes), query digits
-    constexpr int smem = 1024 + kPage * D * (kKStages + kVStages + 2 * kFStages) + (TWO ? 2 : 1) * 2 * kRows * D +
+    // steps of k, of v, of v in fp16 (twice as many bytes), query digits
+    constexpr int smem = 1024 + 2 * kPage * D * (kKStages + kVStages + 2 * kFStages) + 2 * kRows * D +
                          static_cast<int>(sizeof(Control) + sizeof(Seqs));
     static_assert(smem <= 227 * 1024, "shared memory of a block");
-    auto *fn = moe_kv_attend_tc_kernel<D, TWO>;
+    auto *fn = moe_kv_attend_tc_kernel<D>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     LaunchCfg l(dim3(grid), dim3(kThreads), smem, st);
@@ -613,11 +629,9 @@ cudaError_t launch_one(const AttendParams &p, int grid, cudaStream_t st)
 
 }  // namespace
 
-cudaError_t launch_kv_attend_tc(const AttendParams &p, int tile_rows, int num_sms, cudaStream_t st)
+cudaError_t launch_kv_attend_tc(const AttendParams &p, int num_sms, cudaStream_t st)
 {
-    if (p.c.D == 128)
-        return tile_rows == 256 ? launch_one<128, true>(p, num_sms, st) : launch_one<128, false>(p, num_sms, st);
-    return tile_rows == 256 ? launch_one<64, true>(p, num_sms, st) : launch_one<64, false>(p, num_sms, st);
+    return p.c.D == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
 }
 
 }  // namespace moe

@@ -122,7 +122,7 @@ moe::KvParams kv_params(const moe_kv *kv, const moe_kv_batch *b, void *ws)
 // Query rows of a tile of the attention, from the rows of the sequence with the
 // most new tokens: up to 16 the kernel of few rows, whose warps share no rows;
 // above, the tensor-memory kernel, whose rows come by 128.
-int attend_tile_rows(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 128 ? 128 : 256)); }
+int attend_tile_rows(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 128); }
 
 }  // namespace
 
@@ -294,7 +294,7 @@ moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, flo
     const cudaError_t e =
         tile_rows <= 16
             ? moe::launch_kv_attend_rows(p, tile_rows, kv->num_sms, kv->smem_optin, static_cast<cudaStream_t>(stream))
-            : moe::launch_kv_attend_tc(p, tile_rows, kv->num_sms, static_cast<cudaStream_t>(stream));
+            : moe::launch_kv_attend_tc(p, kv->num_sms, static_cast<cudaStream_t>(stream));
     moe::ws_release(tk, e == cudaSuccess);
     return launched(e, "attention launch");
 }

@@ -71,10 +71,10 @@ struct AttendParams {
     float *part;        // [2 * grid] partial results (attend_part_floats each)
     long long timeout_ns;
 };
-constexpr int kAttendMaxRows = 256;  // query rows of the largest tile
+constexpr int kAttendMaxRows = 128;  // query rows of the largest tile
 __host__ __device__ inline size_t attend_part_floats(int D) { return static_cast<size_t>(kAttendMaxRows) * (D + 2); }
 cudaError_t launch_kv_attend_rows(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st);
-// moe_kv_attend_tc.cu: tiles of 128 or 256 rows
-cudaError_t launch_kv_attend_tc(const AttendParams &p, int tile_rows, int num_sms, cudaStream_t st);
+// moe_kv_attend_tc.cu: tiles of 128 rows
+cudaError_t launch_kv_attend_tc(const AttendParams &p, int num_sms, cudaStream_t st);
 
 }  // namespace moe
