@@ -27,6 +27,7 @@ struct Seqs {
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, const AttendParams &p, int *abort_flag)
 {
     uint64_t t0 = 0;  // (reading the timer takes long: not before many tries have failed)
+#pragma unroll 1
     for (uint32_t it = 1; !mbar_test(bar, parity); ++it) {
         if ((it & 31u) != 0) continue;
         if (*reinterpret_cast<volatile int *>(abort_flag)) return;
@@ -177,20 +178,25 @@ __device__ __forceinline__ uint16_t *out_row(const AttendParams &p, int q0, int 
 __device__ __forceinline__ float inv_sum(float gain, float l) { return l > 0.f || l != l ? 1.f / (gain * l) : 0.f; }
 
 // A block's partial result of a tile: slot 0 continues a tile, slot 1 starts
-// one.  Maxima [TR], sums [TR], then the weighted sums [TR][D].
+// one.  Maxima [TR], sums [TR], then the weighted sums [D / 4][TR][4], so that
+// neighbouring rows are neighbours in memory.
 __device__ __forceinline__ float *part_slot(const AttendParams &p, int block, bool starts)
 {
     return p.part + (static_cast<size_t>(block) * 2 + (starts ? 1 : 0)) * attend_part_floats(p.c.D);
 }
 
-// A tile cut between blocks: the last of them to arrive joins the partials of
-// all and writes the output.  NT consumers (the block's first), their partials
-// written.
-template <int D, int NT>
-__device__ __forceinline__ void join_tile(const AttendParams &p, const Segment &s, long long U, int blocks, int TR,
-                                          int rows, int q0, int G, float gain, int *last)
+__device__ __forceinline__ float *part_at(float *part, int TR, int row, int d)
 {
-    const int tid = threadIdx.x;
+    return part + 2 * TR + ((d >> 2) * TR + row) * 4 + (d & 3);
+}
+
+// A tile cut between blocks: the last of them to arrive joins the partials of
+// all and writes the output.  The block's NT consumers, this thread the tid-th of
+// them, their partials written.
+template <int D, int NT, int TR>
+__device__ __forceinline__ void join_tile(const AttendParams &p, const Segment &s, long long U, int blocks, int rows, int q0,
+                                          int G, float gain, int *last, int tid)
+{
     const int c0 = block_of(U, blocks, s.start), c1 = block_of(U, blocks, s.start + s.units - 1);
     __threadfence();
     asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
@@ -202,72 +208,47 @@ __device__ __forceinline__ void join_tile(const AttendParams &p, const Segment &
     asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
     if (!*last) return;
     __threadfence();
-    // a warp takes RU rows at a time (their loads in flight together); a lane
-    // holds one block's factor, and D / 32 columns of the sums
-    constexpr int RU = 4, V = D / 32;
-    const int lane = tid & 31, mine = min(TR, rows - s.tile * TR);
-    for (int r0 = (tid >> 5) * RU; r0 < mine; r0 += NT / 32 * RU) {
-        float M[RU], L[RU], acc[RU][V];
+    // a thread has one row and every (NT / TR)-th group of four columns of it; the
+    // loads of A blocks go out together
+    constexpr int IT = (TR * (D / 4) + NT - 1) / NT, A = IT >= 8 ? 1 : 8 / IT;
+    const int row = tid % TR, g0 = tid / TR, r = s.tile * TR + row;
+    if (r >= rows || g0 >= D / 4) return;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[IT];
 #pragma unroll
-        for (int i = 0; i < RU; ++i) {
-            M[i] = -INFINITY;
-            L[i] = 0.f;
+    for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = c0; k0 <= c1; k0 += A) {
+        float m[A], l[A];
+        float4 v[A][IT];
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[i][j] = 0.f;
-        }
-        for (int k0 = c0; k0 <= c1; k0 += 32) {  // 32 blocks at a time
-            const int kk = k0 + lane;
-            const float *q = part_slot(p, min(kk, c1), min(kk, c1) == c0);
-            float f[RU], lk[RU];
+        for (int x = 0; x < A; ++x) {
+            float *q = part_slot(p, min(k0 + x, c1), min(k0 + x, c1) == c0);
+            m[x] = k0 + x <= c1 ? __ldcg(q + row) : -INFINITY;
+            l[x] = k0 + x <= c1 ? __ldcg(q + TR + row) : 0.f;
 #pragma unroll
-            for (int i = 0; i < RU; ++i) {
-                const int rr = min(r0 + i, mine - 1);
-                f[i] = kk <= c1 ? __ldcg(q + rr) : -INFINITY;
-                lk[i] = kk <= c1 ? __ldcg(q + TR + rr) : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < RU; ++i) {
-                float m = f[i];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                m = fmaxf(m, M[i]);
-                const float ref = m == -INFINITY ? 0.f : m, back = ex2(M[i] - ref);
-                f[i] = ex2(f[i] - ref);
-                float l = lk[i] * f[i];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                L[i] = L[i] * back + l;
-                M[i] = m;
-#pragma unroll
-                for (int j = 0; j < V; ++j) acc[i][j] *= back;
-            }
-            const int m = min(32, c1 - k0 + 1);
-#pragma unroll 4
-            for (int k = 0; k < m; ++k) {
-                const float *o = part_slot(p, k0 + k, k0 + k == c0) + 2 * TR + V * lane;
-#pragma unroll
-                for (int i = 0; i < RU; ++i) {
-                    const float *v = o + static_cast<size_t>(min(r0 + i, mine - 1)) * D;
-                    const float fk = __shfl_sync(0xffffffffu, f[i], k);
-                    if (V == 4) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(v));
-                        acc[i][0] += x.x * fk, acc[i][1] += x.y * fk, acc[i][2] += x.z * fk, acc[i][V - 1] += x.w * fk;
-                    } else {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
-                        acc[i][0] += x.x * fk, acc[i][1] += x.y * fk;
-                    }
-                }
-            }
+            for (int i = 0; i < IT; ++i)
+                v[x][i] = __ldcg(reinterpret_cast<const float4 *>(part_at(q, TR, row, 4 * (g0 + i * (NT / TR)))));
         }
 #pragma unroll
-        for (int i = 0; i < RU; ++i) {
-            if (r0 + i >= mine) break;
-            const float inv = inv_sum(gain, L[i]);
-            uint32_t *o = reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, s.tile * TR + r0 + i) + V * lane);
+        for (int x = 0; x < A; ++x) {
+            const float mn = fmaxf(M, m[x]), ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - ref), f1 = ex2(m[x] - ref);
+            L = L * f0 + l[x] * f1;
+            M = mn;
 #pragma unroll
-            for (int j = 0; j < V; j += 2) o[j / 2] = pack_bf16(acc[i][j] * inv, acc[i][j + 1] * inv);
+            for (int i = 0; i < IT; ++i) {
+                acc[i].x = acc[i].x * f0 + v[x][i].x * f1;
+                acc[i].y = acc[i].y * f0 + v[x][i].y * f1;
+                acc[i].z = acc[i].z * f0 + v[x][i].z * f1;
+                acc[i].w = acc[i].w * f0 + v[x][i].w * f1;
+            }
         }
     }
+    const float inv = inv_sum(gain, L);
+    uint16_t *o = out_row(p, q0, s.h, G, r);
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+        *reinterpret_cast<uint2 *>(o + 4 * (g0 + i * (NT / TR))) =
+            make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
 }
 
 // 2^e * f covers a page's v scale: the exponent that the running maximum adds to

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 b += v.y * f;
             }
             if (!s.whole()) {
-                *reinterpret_cast<float2 *>(part + 2 * TR + rr * D + d) = make_float2(a, b);
+                *reinterpret_cast<float2 *>(part_at(part, TR, rr, d)) = make_float2(a, b);
                 if (d == 0) {
                     part[rr] = mv;
                     part[TR + rr] = lv;
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 *reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, r) + d) = pack_bf16(a * inv, b * inv);
             }
         }
-        if (!s.whole()) join_tile<D, kConsumers>(p, s, U, blocks, TR, rows, q0, G, 256.f, &ct->last);
+        if (!s.whole()) join_tile<D, kConsumers, TR>(p, s, U, blocks, rows, q0, G, 256.f, &ct->last, tid);
     }
 }
 

@@ -210,6 +210,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
 {
     uint32_t d;
@@ -266,18 +272,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
     if (static_cast<int>(blockIdx.x) >= blocks) return;
     const long long u0 = block_start(U, blocks, blockIdx.x), u1 = block_start(U, blocks, blockIdx.x + 1);
-    constexpr int kConverter = kConsumers / 32, kProducer = kConverter + 4, kIssuer = kProducer + 1;  // first warps
+    // first warps of each kind (where several are ready the older issues, and
+    // everything waits for the producer and the issuers)
+    constexpr int kProducer = 0, kIssuer = 1, kConverter = 4, kSoftmax = 8;
     if (wid == kIssuer) tc_alloc(&ct->tmem, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ct->tmem;
 
-    if (wid >= kConverter) {
+    if (wid < kSoftmax) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (wid < kProducer) {
+        if (wid >= kConverter) {
             // ---- v's codes to fp16: rows of a head dim, 64 tokens of a page (128 bytes)
-            const int t = tid - kConsumers;
+            const int t = tid - 32 * kConverter;
             int it = 0;
             for (long long u = u0; u < u1;) {
                 const Segment s = locate(sq, c.B, G, TR, u, u1);
@@ -424,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     } else {
         // ---- softmax: warpgroup w takes the steps n with n % 2 = w, a thread a row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
-        const uint32_t w = wid >> 2;
-        const int row = tid & (kRows - 1);
+        const int ctid = tid - 32 * kSoftmax, row = ctid & (kRows - 1);
+        const uint32_t w = ctid / kRows;
         const uint32_t lanes = static_cast<uint32_t>(wid & 3) << 21;  // this warp's tensor-memory lanes
         const uint32_t ts = tmem + lanes + 128 * w, tp = tmem + lanes + kTmemP + 64 * w, to = tmem + lanes + kTmemO;
         uint32_t n0 = 0;  // steps before the segment
@@ -435,11 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const int steps = (s.pe - s.p0 + 1) / 2;
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last segment is over
             {
-                const int qr = tid >> 1, r = row0 + qr;
-                const float f = put_query<D>(qbuf, qr, tid & 1,
+                const int qr = ctid >> 1, r = row0 + qr;
+                const float f = put_query<D>(qbuf, qr, ctid & 1,
                                              p.q + static_cast<long long>(q0 + r / G) * p.q_stride + (s.h * G + r % G) * D,
                                              r < rows, p.scale_log2);
-                if ((tid & 1) == 0) ct->qs[qr] = f;
+                if ((ctid & 1) == 0) ct->qs[qr] = f;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
@@ -486,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const float *v = &a[2 * y + (j >> 5)][j & 31];
-                            m4[z] = fmaxf(m4[z], fmaxf(v[z], v[z + 4]));
+                            m4[z] = max3(m4[z], v[z], v[z + 4]);
                         }
-                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
                     if (m > -INFINITY) mx = fmaxf(mx, fmaf(m, fs[y], scale_log2(y ? vs.y : vs.x)));
                 }
                 // the reference after the step before, from the other warpgroup
@@ -588,9 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 if (steps > 0) tc_ld16(to + col, v);
                 tc_wait_ld();
                 if (!s.whole()) {
-                    float4 *o = reinterpret_cast<float4 *>(part + 2 * TR + row * D + col);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4 *>(part_at(part, TR, row, col + 4 * j)) =
+                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else if (r < rows) {
                     uint4 *o = reinterpret_cast<uint4 *>(orow + col);
 #pragma unroll
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 }
             }
             tc_fence_before();
-            if (!s.whole()) join_tile<D, kConsumers>(p, s, U, blocks, TR, rows, q0, G, kGain, &ct->last);
+            if (!s.whole()) join_tile<D, kConsumers, TR>(p, s, U, blocks, rows, q0, G, kGain, &ct->last, ctid);
             u += s.p1 - s.p0;
         }
     }
