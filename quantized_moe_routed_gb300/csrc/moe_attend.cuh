@@ -7,9 +7,10 @@
 // A tile is TR query rows (new tokens of one sequence x query heads of one kv
 // head, token after token).  The units are the pages of all (sequence, kv head,
 // tile) in a row; each block (one per SM) takes an equal run of them, so ragged
-// lengths balance without knowing them on the host.  A tile cut by a run's end
-// is joined by the last block that arrives at it, in block order: the same
-// bits every run.
+// lengths balance without knowing them on the host.  Beginning and ending a tile
+// costs time too: COST units without pages stand at the head of each.  A tile cut
+// by a run's end is joined by the last block that arrives at it, in block order:
+// the same bits every run.
 #pragma once
 
 constexpr int kPage = MOE_KV_PAGE;
@@ -44,15 +45,17 @@ __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, co
 // Tokens that row r of a sequence sees (r = new token * group + head).
 __device__ __forceinline__ int row_sees(int len, int n, int G, int r) { return max(len - n + r / G + 1, 0); }
 
-// Units of row tile j: its pages, or one where its last row sees nothing (the
-// tile's zeros still have to be written).
+// Units of row tile j: COST, and its pages, or one where its last row sees
+// nothing (the tile's zeros still have to be written).
+template <int COST>
 __device__ __forceinline__ int tile_units(int len, int n, int G, int TR, int j)
 {
     const int last = min((j + 1) * TR, n * G) - 1;
-    return max(1, (row_sees(len, n, G, last) + kPage - 1) / kPage);
+    return COST + max(1, (row_sees(len, n, G, last) + kPage - 1) / kPage);
 }
 
 // Fill in the sequences and their units; all threads of the block.
+template <int COST>
 __device__ __forceinline__ void plan_units(const AttendParams &p, Seqs &sq, int G, int TR)
 {
     const KvParams &c = p.c;
@@ -66,14 +69,14 @@ __device__ __forceinline__ void plan_units(const AttendParams &p, Seqs &sq, int 
         sq.n[b] = q1 - q0;
         sq.len[b] = len;
         const int rows = (q1 - q0) * G;
-        sq.per_head[b] = rows == 0 ? 0 : (rows <= TR ? tile_units(len, q1 - q0, G, TR, 0) : -1);
+        sq.per_head[b] = rows == 0 ? 0 : (rows <= TR ? tile_units<COST>(len, q1 - q0, G, TR, 0) : -1);
     }
     __syncthreads();
     for (int b = wid; b < c.B; b += blockDim.x >> 5) {  // sequences of several tiles: a warp each
         if (sq.per_head[b] >= 0) continue;
         const int n = sq.n[b], len = sq.len[b], tiles = (n * G + TR - 1) / TR;
         int sum = 0;
-        for (int j = lane; j < tiles; j += 32) sum += tile_units(len, n, G, TR, j);
+        for (int j = lane; j < tiles; j += 32) sum += tile_units<COST>(len, n, G, TR, j);
         sum = __reduce_add_sync(0xffffffffu, sum);
         __syncwarp();
         if (lane == 0) sq.per_head[b] = sum;
@@ -100,14 +103,16 @@ __device__ __forceinline__ void plan_units(const AttendParams &p, Seqs &sq, int 
 
 // A run of units of one tile.
 struct Segment {
-    int b, h, tile, p0, p1;   // pages [p0, p1) of the tile
+    int b, h, tile, p0, p1;   // pages [p0, p1) of the tile (p1 = 0: none of it, nothing to do)
     int pe;                   // p1, or where the sequence's pages end before it
-    int units;                // units of the whole tile
-    long long start;          // first unit of the tile
-    __device__ __forceinline__ bool whole() const { return p0 == 0 && p1 == units; }
+    int pages;                // of the whole tile
+    int units;                // of the run
+    long long start;          // the tile's first unit with a page
+    __device__ __forceinline__ bool whole() const { return p0 == 0 && p1 == pages; }
 };
 
-// The tile that unit u lies in, and the run of it up to unit end.
+// The tile that unit u lies in, and the run of it up to unit end (the whole warp).
+template <int COST>
 __device__ __forceinline__ Segment locate(const Seqs &s, int B, int G, int TR, long long u, long long end)
 {
     Segment g;
@@ -126,11 +131,11 @@ __device__ __forceinline__ Segment locate(const Seqs &s, int B, int G, int TR, l
     int r = rel - g.h * s.per_head[lo];
     const int tiles = (n * G + TR - 1) / TR;
     g.tile = 0;
-    g.units = tile_units(len, n, G, TR, 0);
+    int units = tile_units<COST>(len, n, G, TR, 0);
     if (tiles > 1) {
         const int lane = threadIdx.x & 31;
         for (int j0 = 0; j0 < tiles; j0 += 32) {  // 32 tiles at a time (the whole warp)
-            const int mine = j0 + lane < tiles ? tile_units(len, n, G, TR, j0 + lane) : 0;
+            const int mine = j0 + lane < tiles ? tile_units<COST>(len, n, G, TR, j0 + lane) : 0;
             int sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -141,16 +146,19 @@ __device__ __forceinline__ Segment locate(const Seqs &s, int B, int G, int TR, l
             if (m) {
                 const int l = __ffs(m) - 1;
                 g.tile = j0 + l;
-                g.units = __shfl_sync(0xffffffffu, mine, l);
-                r -= __shfl_sync(0xffffffffu, sum, l) - g.units;
+                units = __shfl_sync(0xffffffffu, mine, l);
+                r -= __shfl_sync(0xffffffffu, sum, l) - units;
                 break;
             }
             r -= __shfl_sync(0xffffffffu, sum, 31);
         }
     }
-    g.start = u - r;
-    g.p0 = r;
-    g.p1 = static_cast<int>(min(static_cast<long long>(g.units), r + (end - u)));
+    const int stop = static_cast<int>(min(static_cast<long long>(units), r + (end - u)));
+    g.start = u - r + COST;
+    g.pages = units - COST;
+    g.units = stop - r;
+    g.p0 = max(0, r - COST);
+    g.p1 = max(0, stop - COST);
     g.pe = max(g.p0, min(g.p1, (len + kPage - 1) / kPage));
     return g;
 }
@@ -197,7 +205,7 @@ template <int D, int NT, int TR>
 __device__ __forceinline__ void join_tile(const AttendParams &p, const Segment &s, long long U, int blocks, int rows, int q0,
                                           int G, float gain, int *last, int tid)
 {
-    const int c0 = block_of(U, blocks, s.start), c1 = block_of(U, blocks, s.start + s.units - 1);
+    const int c0 = block_of(U, blocks, s.start), c1 = block_of(U, blocks, s.start + s.pages - 1);
     __threadfence();
     asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
     if (tid == 0) {

@@ -14,16 +14,17 @@
 // s + ceil(log2(vs)), so that the fp16 weights have their range for what is
 // actually added, whatever the pages' scales.
 //
-// A block's 8 warps take the pages of its run in turn, each with its own
-// maximum, sum and accumulators (16 rows x head dim), and add up at a tile's
-// end in warp order; nothing but the ring of pages couples them.
+// A block's 8 warps take the pages of its run in turn, two warps a page (half its
+// tokens each: the sooner a page is done, the more of the ring is in flight), with
+// their own maximum, sum and accumulators (16 rows x head dim), and add up at a
+// tile's end in warp order; nothing but the ring of pages couples them.
 //
 // Order inside a page is free as long as both products agree: column c of
-// score tile j is token 16 (c / 2) + 2 j + c % 2, which makes a lane's 16
-// weights of a row the 16 consecutive tokens that it reads of a v row, and a
-// lane's k and q elements 32 (head dim 128) or 16 consecutive ones.  k comes by
-// TMA with the 128-byte swizzle, v as it lies; all shared-memory reads are 16
-// bytes wide and free of bank conflicts.
+// score tile j is token 16 (c / 2) + 2 j + c % 2, which makes a lane's weights of
+// a row consecutive tokens that it reads of a v row (8 of 16 a warp), and a lane's
+// k and q elements 32 (head dim 128) or 16 consecutive ones.  k comes by TMA with
+// the 128-byte swizzle, free of bank conflicts; v as it lies, its 8-byte reads
+// two to a bank.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -47,6 +48,10 @@ constexpr int kThreads = kConsumers + 128;  // consumers, and a warpgroup whose 
 // the block is launched with (384 threads of 168).
 constexpr int kConsumerRegs = 216, kProducerRegs = 72;
 
+// What beginning and ending a tile costs, in pages.
+constexpr int kTileCost = 4;
+constexpr int kPageWarps = 2;  // warps that share a page: tokens 8 h .. 8 h + 7 of every 16
+
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
     float ks[kMaxStages], vs[kMaxStages];  // scales of the stage's page; ks < 0: no such page
@@ -68,6 +73,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
     constexpr int TR = 8 * NX;                  // query rows of a tile
     constexpr int KS = D / 16;                  // K steps of the first product
     constexpr int DT = D / 8;                   // N tiles of the second
+    constexpr int NJ = 8 / kPageWarps;          // score tiles of a warp
     constexpr int kStage = 2 * kPage * D;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -82,13 +88,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
         ct->abort = 0;
         for (int i = 0; i < NS; ++i) {
             mbar_init(&ct->full[i], 1);
-            mbar_init(&ct->empty[i], 1);
+            mbar_init(&ct->empty[i], kPageWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     grid_wait();
     grid_release();
-    plan_units(p, sq, G, TR);
+    plan_units<kTileCost>(p, sq, G, TR);
     const long long U = sq.cum[c.B];
     const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
     if (static_cast<int>(blockIdx.x) >= blocks) return;
@@ -101,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
         int it = 0;
         const uint64_t pol = policy_evict_first();
         for (long long u = u0; u < u1;) {
-            const Segment s = locate(sq, c.B, G, TR, u, u1);
+            const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
             for (int pb = s.p0; pb < s.pe; pb += 32) {
                 const PageInfo pi = load_pages(c, s, pb);
                 const int m = min(32, s.pe - pb);
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                     __syncwarp();
                 }
             }
-            u += s.p1 - s.p0;
+            u += s.units;
         }
         // every copy is waited for by the warp that uses it, unless it gave up:
         // no block ends with a copy into its shared memory in flight
@@ -148,7 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
     int it0 = 0;  // pages of this block before the segment
     for (long long u = u0; u < u1;) {
-        const Segment s = locate(sq, c.B, G, TR, u, u1);
+        const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
+        u += s.units;
+        if (s.p1 == 0) continue;
         const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b];
 
         // q: fp16 of the lane's D / 4 elements of rows g and g + 8 of the tile
@@ -197,7 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
-        for (int pg = s.p0 + wid; pg < s.pe; pg += kWarps) {
+        const int half = wid % kPageWarps;
+        for (int pg = s.p0 + wid / kPageWarps; pg < s.pe; pg += kWarps / kPageWarps) {
             const int it = it0 + pg - s.p0, st = it % NS;
             wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);
             __syncwarp();
@@ -208,18 +217,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 if (lane == 0) mbar_arrive(&ct->empty[st]);
                 continue;
             }
-            // scores: K step by K step over eight independent accumulators
-            float sc[8][4];
+            // scores: K step by K step over independent accumulators
+            float sc[NJ][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
 #pragma unroll
             for (int i = 0; i < KS / 4; ++i) {
-                uint4 w[8];
+                uint4 w[NJ];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int tok = 16 * (g >> 1) + 2 * j + (g & 1);
+                for (int j = 0; j < NJ; ++j) {
+                    const int tok = 16 * (g >> 1) + 2 * (NJ * half + j) + (g & 1);
                     const int gr = D == 128 ? ((2 * t4 + i) ^ (tok & 7)) : t4;
                     w[j] = *reinterpret_cast<const uint4 *>(kp + tok * D + gr * 16);
                 }
@@ -227,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 for (int y = 0; y < 4; ++y) {
                     const int a = 2 * (4 * i + y);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < NJ; ++j) {
                         const uint32_t k4 = u4w(w[j], y);
                         mma16816(sc[j], qf[0][a], qf[1][a], qf[0][a + 1], qf[1][a + 1],
                                  e4m3x2_to_f16x2(static_cast<uint16_t>(k4)), e4m3x2_to_f16x2(static_cast<uint16_t>(k4 >> 16)));
@@ -244,11 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 mx[x] = -INFINITY;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int x = 0; x < 2 * NX; ++x) {
                     sc[j][x] *= fs[x >> 1];
-                    if (edge && pg * kPage + 16 * t4 + 2 * j + (x & 1) >= sees[x >> 1]) sc[j][x] = -INFINITY;
+                    if (edge && pg * kPage + 16 * t4 + 2 * (NJ * half + j) + (x & 1) >= sees[x >> 1]) sc[j][x] = -INFINITY;
                     mx[x >> 1] = fmaxf(mx[x >> 1], sc[j][x]);
                 }
             float ref[NX], alpha[NX];
@@ -271,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
 #pragma unroll
                     for (int x = 0; x < 2 * NX; ++x) o[i][x] *= alpha[x >> 1];
             }
-            uint32_t pf[2][8];  // weights: [row][token pair]
+            uint32_t pf[2][NJ];  // weights: [row][token pair]
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (x < NX) {
@@ -287,15 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 }
 #pragma unroll
             for (int i0 = 0; i0 < DT; i0 += 8) {
-                uint4 w[8];
+                uint2 w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    w[i] = *reinterpret_cast<const uint4 *>(vp + (8 * (i0 + i) + g) * kPage + 16 * t4);
+                    w[i] = *reinterpret_cast<const uint2 *>(vp + (8 * (i0 + i) + g) * kPage + 16 * t4 + 8 * half);
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint32_t v4 = u4w(w[i], y);
+                        const uint32_t v4 = y ? w[i].y : w[i].x;
                         mma16816(o[i0 + i], pf[0][2 * y], pf[1][2 * y], pf[0][2 * y + 1], pf[1][2 * y + 1],
                                  e4m3x2_to_f16x2(static_cast<uint16_t>(v4)), e4m3x2_to_f16x2(static_cast<uint16_t>(v4 >> 16)));
                     }
@@ -304,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
             if (lane == 0) mbar_arrive(&ct->empty[st]);
         }
         it0 += s.pe - s.p0;
-        u += s.p1 - s.p0;
 
         // ---- the warps' sums to shared memory, added in warp order
         float *mo = mrg, *mm = mrg + kWarps * TR * (D + 4), *ml = mm + kWarps * TR;

@@ -59,6 +59,9 @@ constexpr float kGain = 64.f;    // of the weights
 constexpr float kSlack = 8.f;    // how far a step may exceed the reference (64 * 2^8 is inside fp16)
 // Tensor memory: warpgroup b's S at 128 b, its P at 256 + 64 b, O at 384.
 constexpr int kTmemCols = 512, kTmemP = 256, kTmemO = 384;
+// What beginning and ending a tile (queries, joining, filling and draining) costs,
+// in pages: about 14000 cycles against 1050 a page.
+constexpr int kTileCost = 12;
 constexpr int kKStages = 4, kVStages = 3, kFStages = 2;  // steps of k, of v, of v in fp16
 constexpr int kScales = 8;       // steps whose scales are kept: more than a softmax lags behind the producer
 
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     }
     grid_wait();
     grid_release();
-    plan_units(p, sq, G, TR);
+    plan_units<kTileCost>(p, sq, G, TR);
     const long long U = sq.cum[c.B];
     const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
     if (static_cast<int>(blockIdx.x) >= blocks) return;
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const int t = tid - 32 * kConverter;
             int it = 0;
             for (long long u = u0; u < u1;) {
-                const Segment s = locate(sq, c.B, G, TR, u, u1);
+                const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
                 const int end = it + (s.pe - s.p0 + 1) / 2;
                 for (; it < end; ++it) {
                     const int vs = it % kVStages, f = it % kFStages;
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     mbar_arrive(&ct->f_full[f]);
                     mbar_arrive(&ct->v_empty[vs]);
                 }
-                u += s.p1 - s.p0;
+                u += s.units;
             }
         } else if (wid == kProducer) {
             // ---- producer: two pages a step; an odd last page comes twice (the second
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             int it = 0;
             const uint64_t pol = policy_evict_last();  // other tiles read the page too
             for (long long u = u0; u < u1;) {
-                const Segment s = locate(sq, c.B, G, TR, u, u1);
+                const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
                 for (int pb = s.p0; pb < s.pe; pb += 32) {
                     const PageInfo pi = load_pages(c, s, pb);
                     const int m = min(32, s.pe - pb);
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                         __syncwarp();
                     }
                 }
-                u += s.p1 - s.p0;
+                u += s.units;
             }
             if (lane == 0 && aborted()) {
                 // no block ends with a copy into its shared memory in flight
@@ -382,14 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const uint32_t qd = desc_lo(smem_u32(qbuf)), kd = desc_lo(smem_u32(kbuf)), fd = desc_lo(smem_u32(fbuf));
             int slot = 0, nseg = 0;      // buffer of the next step; segments so far
             uint32_t phase = 0, n = 0;   // of that buffer; steps so far
-            for (long long u = u0; u < u1; ++nseg) {
-                const Segment s = locate(sq, c.B, G, TR, u, u1);
+            for (long long u = u0; u < u1;) {
+                const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
                 const int steps = (s.pe - s.p0 + 1) / 2;
-                u += s.p1 - s.p0;
+                u += s.units;
                 __syncwarp();
-                if (lane != 0) continue;
+                if (lane != 0 || s.p1 == 0) continue;
                 if (scores) {
-                    wait_or_abort(&ct->q_ready, nseg & 1, p, &ct->abort);
+                    wait_or_abort(&ct->q_ready, nseg++ & 1, p, &ct->abort);
                     for (int i = 0; i < steps; ++i, ++n) {
                         const uint32_t b = n & 1, d = tmem + 128 * b, k = kd + slot * (kStep / 16);
                         wait_or_abort(&ct->k_full[slot], phase, p, &ct->abort);
@@ -438,7 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
         const uint32_t ts = tmem + lanes + 128 * w, tp = tmem + lanes + kTmemP + 64 * w, to = tmem + lanes + kTmemO;
         uint32_t n0 = 0;  // steps before the segment
         for (long long u = u0; u < u1;) {
-            const Segment s = locate(sq, c.B, G, TR, u, u1);
+            const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
+            u += s.units;
+            if (s.p1 == 0) continue;
             const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b], row0 = s.tile * TR;
             const int steps = (s.pe - s.p0 + 1) / 2;
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last segment is over
@@ -612,7 +617,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             }
             tc_fence_before();
             if (!s.whole()) join_tile<D, kConsumers, TR>(p, s, U, blocks, rows, q0, G, kGain, &ct->last, ctid);
-            u += s.p1 - s.p0;
         }
     }
     __syncwarp();

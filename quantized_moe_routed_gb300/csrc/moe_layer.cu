@@ -281,8 +281,8 @@ moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, flo
     if (!aligned(o_dev, 16)) return fail(MOE_ERR_MISALIGNED, "o needs 16-byte alignment");
     const long long G = kv->d.q_heads / kv->d.kv_heads;
     const int tile_rows = attend_tile_rows(batch->max_q * G);
-    // the kernels count the units of a sequence (pages of all its tiles) in 32 bits
-    if (batch->N * G / tile_rows + 1 > 0x7FFFFFFFLL / kv->d.kv_heads / batch->max_pages)
+    // the kernels count the units of a sequence (pages of all its tiles, and up to 16 more a tile) in 32 bits
+    if (batch->N * G / tile_rows + 1 > 0x7FFFFFFFLL / kv->d.kv_heads / (batch->max_pages + 16))
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "N=%d new tokens over max_pages=%d pages are too many for one step", batch->N,
                     batch->max_pages);
     uint8_t *ws = static_cast<uint8_t *>(ws_dev);
