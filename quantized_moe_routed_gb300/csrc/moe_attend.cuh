@@ -207,12 +207,14 @@ __device__ __forceinline__ void join_tile(const AttendParams &p, const Segment &
 {
     const int c0 = block_of(U, blocks, s.start), c1 = block_of(U, blocks, s.start + s.pages - 1);
     __threadfence();
+    __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
     if (tid == 0) {
         const uint32_t old = atom_add_acqrel_gpu(p.count + c0, 1u);
         *last = old == static_cast<uint32_t>(c1 - c0);
         if (*last) p.count[c0] = 0u;
     }
+    __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
     if (!*last) return;
     __threadfence();

@@ -51,6 +51,11 @@ constexpr int kConsumerRegs = 216, kProducerRegs = 72;
 // What beginning and ending a tile costs, in pages.
 constexpr int kTileCost = 4;
 constexpr int kPageWarps = 2;  // warps that share a page: tokens 8 h .. 8 h + 7 of every 16
+// Page n of a block is group n % kGroups's, in stage n % NS.  NS is a multiple of
+// kGroups, so a stage has one group for good: with another it could be waited
+// for a phase ahead (a group can be done with its pages while an earlier page of
+// another group is still on its way), and a barrier only tells neighbouring phases apart.
+constexpr int kGroups = kWarps / kPageWarps;
 
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -65,6 +70,9 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
     return d;
 }
 
+// Columns of the weighted sums that the warps add at a time: what fits beside the ring.
+__host__ __device__ constexpr int merge_cols(int D, int NX) { return D < 64 / NX ? D : 64 / NX; }
+
 // NX: query rows of a tile / 8 (1 or 2).  Shared memory: ring of stages (k page,
 // v page), the control block, the sequences, the warps' results.
 template <int D, int NX>
@@ -74,6 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
     constexpr int KS = D / 16;                  // K steps of the first product
     constexpr int DT = D / 8;                   // N tiles of the second
     constexpr int NJ = 8 / kPageWarps;          // score tiles of a warp
+    constexpr int CC = merge_cols(D, NX);
     constexpr int kStage = 2 * kPage * D;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
         const int half = wid % kPageWarps;
-        for (int pg = s.p0 + wid / kPageWarps; pg < s.pe; pg += kWarps / kPageWarps) {
+        for (int pg = s.p0 + (wid / kPageWarps + kGroups - it0 % kGroups) % kGroups; pg < s.pe; pg += kGroups) {
             const int it = it0 + pg - s.p0, st = it % NS;
             wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);
             __syncwarp();
@@ -314,48 +323,57 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
         }
         it0 += s.pe - s.p0;
 
-        // ---- the warps' sums to shared memory, added in warp order
-        float *mo = mrg, *mm = mrg + kWarps * TR * (D + 4), *ml = mm + kWarps * TR;
-        asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last segment's reads are over
+        // ---- the warps' sums to shared memory, added in warp order, CC columns at a time
+        float *mo = mrg, *mm = mrg + kWarps * TR * (CC + 4), *ml = mm + kWarps * TR;
+        float *part = part_slot(p, blockIdx.x, s.p0 == 0);
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
-            const int rr = wid * TR + 8 * x + g;
             l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
             l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-            if (t4 == 0) {
-                mm[rr] = m[x];
-                ml[rr] = l[x];
-            }
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-                *reinterpret_cast<float2 *>(mo + rr * (D + 4) + 8 * i + 2 * t4) = make_float2(o[i][2 * x], o[i][2 * x + 1]);
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-        float *part = part_slot(p, blockIdx.x, s.p0 == 0);
-        for (int i = tid; i < TR * (D / 2); i += kConsumers) {
-            const int rr = i / (D / 2), d = 2 * (i % (D / 2)), r = s.tile * TR + rr;
-            float mv = -INFINITY, lv = 0.f, a = 0.f, b = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) mv = fmaxf(mv, mm[k * TR + rr]);
-            const float ref = mv == -INFINITY ? 0.f : mv;
+        for (int c0 = 0; c0 < D; c0 += CC) {
+            __syncwarp();
+            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last reads are over
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const int q = k * TR + rr;
-                const float f = ex2(mm[q] - ref);
-                const float2 v = *reinterpret_cast<const float2 *>(mo + q * (D + 4) + d);
-                lv += ml[q] * f;
-                a += v.x * f;
-                b += v.y * f;
-            }
-            if (!s.whole()) {
-                *reinterpret_cast<float2 *>(part_at(part, TR, rr, d)) = make_float2(a, b);
-                if (d == 0) {
-                    part[rr] = mv;
-                    part[TR + rr] = lv;
+            for (int x = 0; x < NX; ++x) {
+                const int rr = wid * TR + 8 * x + g;
+                if (t4 == 0) {
+                    mm[rr] = m[x];
+                    ml[rr] = l[x];
                 }
-            } else if (r < rows) {
-                const float inv = inv_sum(256.f, lv);
-                *reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, r) + d) = pack_bf16(a * inv, b * inv);
+#pragma unroll
+                for (int i = 0; i < CC / 8; ++i)
+                    *reinterpret_cast<float2 *>(mo + rr * (CC + 4) + 8 * i + 2 * t4) =
+                        make_float2(o[c0 / 8 + i][2 * x], o[c0 / 8 + i][2 * x + 1]);
+            }
+            __syncwarp();
+            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+            for (int i = tid; i < TR * (CC / 2); i += kConsumers) {
+                const int rr = i / (CC / 2), cc = 2 * (i % (CC / 2)), d = c0 + cc, r = s.tile * TR + rr;
+                float mv = -INFINITY, lv = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) mv = fmaxf(mv, mm[k * TR + rr]);
+                const float ref = mv == -INFINITY ? 0.f : mv;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {
+                    const int q = k * TR + rr;
+                    const float f = ex2(mm[q] - ref);
+                    const float2 v = *reinterpret_cast<const float2 *>(mo + q * (CC + 4) + cc);
+                    lv += ml[q] * f;
+                    a += v.x * f;
+                    b += v.y * f;
+                }
+                if (!s.whole()) {
+                    *reinterpret_cast<float2 *>(part_at(part, TR, rr, d)) = make_float2(a, b);
+                    if (d == 0) {
+                        part[rr] = mv;
+                        part[TR + rr] = lv;
+                    }
+                } else if (r < rows) {
+                    const float inv = inv_sum(256.f, lv);
+                    *reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, r) + d) = pack_bf16(a * inv, b * inv);
+                }
             }
         }
         if (!s.whole()) join_tile<D, kConsumers, TR>(p, s, U, blocks, rows, q0, G, 256.f, &ct->last, tid);
@@ -366,8 +384,8 @@ template <int D, int NX>
 cudaError_t launch_one(const AttendParams &p, int grid, int smem_optin, cudaStream_t st)
 {
     constexpr int kStage = 2 * kPage * D;
-    const int fixed = 1024 + static_cast<int>(sizeof(Control) + sizeof(Seqs)) + kWarps * 8 * NX * (D + 6) * 4;
-    const int ns = std::min(kMaxStages, (smem_optin - fixed) / kStage);
+    const int fixed = 1024 + static_cast<int>(sizeof(Control) + sizeof(Seqs)) + kWarps * 8 * NX * (merge_cols(D, NX) + 6) * 4;
+    const int ns = std::min(kMaxStages, (smem_optin - fixed) / kStage) / kGroups * kGroups;
     const int smem = fixed + ns * kStage;
     auto *fn = moe_kv_attend_kernel<D, NX>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

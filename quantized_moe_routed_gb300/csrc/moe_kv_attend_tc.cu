@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             if (s.p1 == 0) continue;
             const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b], row0 = s.tile * TR;
             const int steps = (s.pe - s.p0 + 1) / 2;
+            __syncwarp();
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last segment is over
             {
                 const int qr = ctid >> 1, r = row0 + qr;
@@ -457,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             mbar_arrive(&ct->q_ready);
+            __syncwarp();
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             const int r = row0 + row;
             const int sees = r < rows ? row_sees(len, n, G, r) : 0;
@@ -573,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             // ---- the result: o / 64 in tensor memory, the last reference, the sums
             ct->l[w][row] = l;
             ct->lref[w][row] = lref;
+            __syncwarp();
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             n0 += steps;
             float ref = -INFINITY, lsum = 0.f;
