@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 128;  // consumers, and a warpgroup whose first warp is the producer
+constexpr int kThreads = kConsumers + 128;  // consumers, and a warpgroup of producers
 // Registers a thread of the two kinds keeps: 256 * 216 + 128 * 72 = 64512, what
 // the block is launched with (384 threads of 168).
 constexpr int kConsumerRegs = 216, kProducerRegs = 72;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
     if (tid == 0) {
         ct->abort = 0;
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&ct->full[i], 1);
+            mbar_init(&ct->full[i], 2);  // k and v
             mbar_init(&ct->empty[i], kPageWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -111,8 +111,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
 
     if (wid >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        if (wid > kWarps) return;
-        // ---- producer: a page a stage
+        // ---- producers: a page a stage; warps 0 and 2 bring k, 1 and 3 v, of even and
+        // odd pages (one thread's issue alone would bound the kernel)
+        const bool values = wid & 1;
+        const int odd = (wid - kWarps) >> 1;
         int it = 0;
         const uint64_t pol = policy_evict_first();
         for (long long u = u0; u < u1;) {
@@ -120,31 +122,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
             for (int pb = s.p0; pb < s.pe; pb += 32) {
                 const PageInfo pi = load_pages(c, s, pb);
                 const int m = min(32, s.pe - pb);
-                for (int i = 0; i < m; ++i, ++it) {
-                    const int st = it % NS;
+                for (int i = (it & 1) ^ odd; i < m; i += 2) {
+                    const int n = it + i, st = n % NS;
                     const int pid = __shfl_sync(0xffffffffu, pi.id, i);
-                    const float ks = __shfl_sync(0xffffffffu, pi.ks, i), vs = __shfl_sync(0xffffffffu, pi.vs, i);
+                    const float scale = __shfl_sync(0xffffffffu, values ? pi.vs : pi.ks, i);
                     if (lane == 0) {
-                        if (it >= NS) wait_or_abort(&ct->empty[st], (it / NS - 1) & 1, p, &ct->abort);
+                        if (n >= NS) wait_or_abort(&ct->empty[st], (n / NS - 1) & 1, p, &ct->abort);
                         if (*reinterpret_cast<volatile int *>(&ct->abort) == 0) {
-                            ct->ks[st] = ks;
-                            ct->vs[st] = vs;
+                            (values ? ct->vs : ct->ks)[st] = scale;
+                            uint8_t *dst = smem + st * kStage + (values ? kPage * D : 0);
+                            const size_t ph = static_cast<size_t>(max(pid, 0)) * c.kv_heads + s.h;
                             if (pid < 0) {
                                 mbar_arrive(&ct->full[st]);
                             } else {
-                                mbar_expect_tx(&ct->full[st], kStage);
-                                uint8_t *dst = smem + st * kStage;
-                                const size_t ph = static_cast<size_t>(pid) * c.kv_heads + s.h;
-                                if (D == 128)
-                                    tma2d(dst, &c.tm_k, 0, static_cast<int>(ph * kPage), &ct->full[st], pol);
+                                mbar_expect_tx(&ct->full[st], kPage * D);
+                                if (values || D == 64)
+                                    bulk_g2s(dst, (values ? c.v : c.k) + ph * (kPage * D), kPage * D, &ct->full[st], pol);
                                 else
-                                    bulk_g2s(dst, c.k + ph * (kPage * D), kPage * D, &ct->full[st], pol);
-                                bulk_g2s(dst + kPage * D, c.v + ph * (kPage * D), kPage * D, &ct->full[st], pol);
+                                    tma2d(dst, &c.tm_k, 0, static_cast<int>(ph * kPage), &ct->full[st], pol);
                             }
                         }
                     }
                     __syncwarp();
                 }
+                it += m;
             }
             u += s.units;
         }
