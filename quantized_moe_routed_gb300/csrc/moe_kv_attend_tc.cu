@@ -26,8 +26,8 @@
 // steps in turn (a thread a row), each with its own S and P in tensor memory; the
 // scores of a warpgroup's next step are computed once it has read this one's,
 // and P V during the following softmax.  Only the reference goes from step to step, as
-// soon as a step's maxima are known.  One warp brings pages, one thread issues
-// the products for S and one those for O, a warpgroup converts v.  With two row
+// soon as a step's maxima are known.  Two threads bring pages, one issues the
+// products for S and one those for O, a warpgroup converts v.  With two row
 // tiles a block sharing k and v, tensor memory leaves no room for this (S and P in one
 // place): the softmax then waits for the chain from its weights over P V to the next
 // scores, 580 us for 2048 x 16384 tokens and 32 heads.
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     const long long u0 = block_start(U, blocks, blockIdx.x), u1 = block_start(U, blocks, blockIdx.x + 1);
     // first warps of each kind (where several are ready the older issues, and
     // everything waits for the producer and the issuers)
-    constexpr int kProducer = 0, kIssuer = 1, kConverter = 4, kSoftmax = 8;
+    constexpr int kProducer = 0, kIssuer = 2, kConverter = 4, kSoftmax = 8;
     if (wid == kIssuer) tc_alloc(&ct->tmem, kTmemCols);
     tc_fence_before();
     __syncthreads();
@@ -319,10 +319,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 }
                 u += s.units;
             }
-        } else if (wid == kProducer) {
-            // ---- producer: two pages a step; an odd last page comes twice (the second
-            // copy is behind every row's mask)
-            int it = 0;
+        } else if (wid < kIssuer) {
+            // ---- producers, one of k and one of v: two pages a step; an odd last page
+            // comes twice (the second copy is behind every row's mask)
+            const bool values = wid != kProducer;
+            const int stages = values ? kVStages : kKStages;
+            uint64_t *full = values ? ct->v_full : ct->k_full, *empty = values ? ct->v_empty : ct->k_empty;
+            int it = 0, st = 0;
+            uint32_t phase = 1;
             const uint64_t pol = policy_evict_last();  // other tiles read the page too
             for (long long u = u0; u < u1;) {
                 const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
@@ -330,7 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     const PageInfo pi = load_pages(c, s, pb);
                     const int m = min(32, s.pe - pb);
                     for (int i = 0; i < m; i += 2, ++it) {
-                        const int ks = it % kKStages, vs = it % kVStages, sc = it % kScales;
                         int ph[2];
                         float pks[2], pvs[2];
 #pragma unroll
@@ -342,26 +345,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                             pvs[x] = __shfl_sync(0xffffffffu, pi.vs, src);
                         }
                         if (lane == 0) {
-                            if (it >= kKStages) wait_or_abort(&ct->k_empty[ks], (it / kKStages - 1) & 1, p, &ct->abort);
+                            if (it >= stages) wait_or_abort(&empty[st], phase, p, &ct->abort);
                             if (!aborted()) {
-                                mbar_expect_tx(&ct->k_full[ks], kStep);
+                                uint8_t *dst = (values ? vbuf : kbuf) + st * kStep;
+                                mbar_expect_tx(&full[st], kStep);
+                                if (values) {
 #pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    ct->ks[sc][x] = pks[x];
-                                    ct->vs[sc][x] = pvs[x];
-                                    tma2d(kbuf + ks * kStep + x * kPageBytes, &c.tm_k, 0, ph[x] * kPage, &ct->k_full[ks], pol);
+                                    for (int x = 0; x < 2; ++x)
+                                        bulk_g2s(dst + x * kPageBytes, c.v + static_cast<size_t>(ph[x]) * kPageBytes, kPageBytes,
+                                                 &full[st], pol);
+                                } else {
+                                    const int sc = it % kScales;
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) {
+                                        ct->ks[sc][x] = pks[x];
+                                        ct->vs[sc][x] = pvs[x];
+                                        tma2d(dst + x * kPageBytes, &c.tm_k, 0, ph[x] * kPage, &full[st], pol);
+                                    }
+                                    mbar_arrive(&ct->sc_full[sc]);
                                 }
-                                mbar_arrive(&ct->sc_full[sc]);
-                            }
-                            if (it >= kVStages) wait_or_abort(&ct->v_empty[vs], (it / kVStages - 1) & 1, p, &ct->abort);
-                            if (!aborted()) {
-                                mbar_expect_tx(&ct->v_full[vs], kStep);
-#pragma unroll
-                                for (int x = 0; x < 2; ++x)
-                                    bulk_g2s(vbuf + vs * kStep + x * kPageBytes, c.v + static_cast<size_t>(ph[x]) * kPageBytes,
-                                             kPageBytes, &ct->v_full[vs], pol);
                             }
                         }
+                        if (++st == stages) st = 0, phase ^= 1;
                         __syncwarp();
                     }
                 }
@@ -370,12 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             if (lane == 0 && aborted()) {
                 // no block ends with a copy into its shared memory in flight
                 const uint64_t t0 = gtimer();
-                auto over = [&] { return static_cast<long long>(gtimer() - t0) >= p.timeout_ns; };
-                for (int j = max(it - kKStages, 0); j < it; ++j)
-                    while (!mbar_test(&ct->k_full[j % kKStages], (j / kKStages) & 1) && !over()) {
-                    }
-                for (int j = max(it - kVStages, 0); j < it; ++j)
-                    while (!mbar_test(&ct->v_full[j % kVStages], (j / kVStages) & 1) && !over()) {
+                for (int j = max(it - stages, 0); j < it; ++j)
+                    while (!mbar_test(&full[j % stages], (j / stages) & 1) &&
+                           static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
                     }
             }
         } else if (wid == kIssuer || wid == kIssuer + 1) {
