@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_nvfp4.so")
 SOURCES = ("moe_kernels.cu", "moe_tc.cu", "moe_small.cu", "moe_gemv.cu", "moe_route.cu", "moe_abi.cu",
-           "moe_norm.cu", "moe_linear.cu", "moe_kv_append.cu", "moe_kv_attend.cu", "moe_kv_attend_tc.cu",
+           "moe_norm.cu", "moe_linear.cu", "moe_linear_tc.cu", "moe_kv_append.cu", "moe_kv_attend.cu", "moe_kv_attend_tc.cu",
            "moe_layer.cu")
 HEADERS = ("moe_internal.h", "moe_device.cuh", "moe_tcgen05.cuh", "moe_host.h", "moe_layer_internal.h",
            "moe_layer_device.cuh", "moe_attend.cuh")

@@ -1,7 +1,7 @@
 // moe_layer.cu -- host side of the C ABI declared in include/moe_layer.h:
 // argument validation, the cache handle, its workspace, launches.  The
-// computation runs in moe_norm.cu, moe_linear.cu, moe_kv_append.cu and
-// moe_kv_attend.cu.
+// computation runs in moe_norm.cu, moe_linear.cu, moe_linear_tc.cu,
+// moe_kv_append.cu, moe_kv_attend.cu and moe_kv_attend_tc.cu.
 #include "moe_layer.h"
 #include "moe_host.h"
 #include "moe_internal.h"
@@ -124,6 +124,20 @@ moe::KvParams kv_params(const moe_kv *kv, const moe_kv_batch *b, void *ws)
 // above, the tensor-memory kernel, whose rows come by 128.
 int attend_tile_rows(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 128); }
 
+// Whether the tensor-core kernel takes a product: where its loads may go, and where
+// the rows and the length give it enough work past what it takes to begin (every
+// block reads all of x first).  Measured, it against the others, at K = 4096: 8
+// tokens, 64 rows an SM 14.7 / 12.4 us, 96 rows 14.9 / 16.5, 512 rows 37 / 44; 24
+// tokens, 64 rows 20.2 / 20.2, 128 rows 21 / 28, 512 rows 43 / 76; 64 tokens, 64
+// rows 41 / 55.  At K = 1024: 8 tokens, 128 rows 9.1 / 7.5, 256 rows 10.5 / 10.3;
+// 24 tokens, 128 rows 10.4 / 10.7.
+bool linear_on_tensor_cores(const moe::LinearParams &p, int sms)
+{
+    const int rows = p.N / sms;
+    return p.K % 256 == 0 && aligned(p.s, 16) && rows >= 64 &&
+           static_cast<long long>(rows) * p.K >= (p.T > 16 ? 128 : 320) * 1024;
+}
+
 }  // namespace
 
 extern "C" {
@@ -175,7 +189,15 @@ moe_status_t moe_linear(const uint8_t *q_dev, const uint8_t *s_dev, const float 
     const moe_status_t st = query_device(-1, &dev);
     if (st != MOE_OK) return st;
     const moe::LinearParams p{q_dev, s_dev, ts_dev, static_cast<const uint16_t *>(x_dev), x_stride, y_dev, N, K, T, y_bf16};
-    return launched(moe::launch_linear(p, dev.sms, static_cast<cudaStream_t>(stream)), "linear launch");
+    if (!linear_on_tensor_cores(p, dev.sms))
+        return launched(moe::launch_linear(p, dev.sms, static_cast<cudaStream_t>(stream)), "linear launch");
+    static const long long limit = moe::wait_limit_ns();
+    if (!moe::encoder()) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const moe::LinearTcPlan plan = moe::linear_tc_plan(p, dev.sms);
+    moe::LinearTcParams tp{{}, p, plan.rows, plan.tiles, limit};
+    const CUresult r = moe::encode_rows(&tp.tm_q, const_cast<uint8_t *>(q_dev), N, K / 2, 128, plan.rows, 128);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "tensor-map encoding failed (CUresult %d)", static_cast<int>(r));
+    return launched(moe::launch_linear_tc(tp, plan.blocks, static_cast<cudaStream_t>(stream)), "linear launch");
 }
 
 moe_status_t moe_kv_create(const moe_kv_desc *desc, moe_kv_t *out)

@@ -37,6 +37,19 @@ struct LinearParams {
 constexpr int kLinearMaxT = 24;  // tokens of one pass over the weights
 cudaError_t launch_linear(const LinearParams &p, int num_sms, cudaStream_t st);
 
+// moe_linear_tc.cu: many rows, K a multiple of 256, s and its rows 16-byte aligned
+struct LinearTcPlan {
+    int rows, tiles, blocks;  // rows of a tile, tiles of a block, blocks along the rows
+};
+struct LinearTcParams {
+    CUtensorMap tm_q;  // boxes of 128 bytes, swizzled, plan.rows high
+    LinearParams l;
+    int rows, tiles;
+    long long timeout_ns;
+};
+LinearTcPlan linear_tc_plan(const LinearParams &p, int num_sms);
+cudaError_t launch_linear_tc(const LinearTcParams &p, int blocks, cudaStream_t st);
+
 // The cache's pages, and one step's sequences (fields as in moe_layer.h).
 struct KvParams {
     CUtensorMap tm_k;  // a page's k as 64 rows of head_dim bytes, swizzled over the row (128 or 64 bytes)

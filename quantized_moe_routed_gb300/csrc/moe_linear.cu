@@ -2,7 +2,8 @@
 //
 //   y[t, n] = ts[n] * sum_k E2M1(q[n, k]) * E4M3(s[n, k/16]) * x[t, k]
 //
-// The weights are read once for up to 24 tokens, so their bytes bound it.
+// The weights are read once for up to 24 tokens, so their bytes bound it.  (Weights
+// of many rows: moe_linear_tc.cu.)
 // They go from global memory to registers (16 bytes a lane, the next loads in
 // flight while these are used), become fp16 there (E2M1 times E4M3 is exact in
 // fp16) and are the A operand of mma.sync m16n8k16; tokens are the N axis.

@@ -126,7 +126,8 @@ def test_rope_table_on_the_host():
         layer.rope_table(5, 8, inv_freq=[1.0, 2.0], device="cpu")
 
 
-@pytest.mark.parametrize("unit,regs", [("moe_norm.cu", 128), ("moe_linear.cu", 128), ("moe_kv_append.cu", 64),
+@pytest.mark.parametrize("unit,regs", [("moe_norm.cu", 128), ("moe_linear.cu", 128), ("moe_linear_tc.cu", 128),
+                                       ("moe_kv_append.cu", 64),
                                        ("moe_kv_attend.cu", 168), ("moe_kv_attend_tc.cu", 128)])
 def test_kernels_fit_their_registers(unit, regs):
     # blocks of 512 threads have 128 registers a thread, of 384 have 168; two
