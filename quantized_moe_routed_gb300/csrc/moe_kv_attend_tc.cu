@@ -60,8 +60,8 @@ constexpr float kSlack = 8.f;    // how far a step may exceed the reference (64 
 // Tensor memory: warpgroup b's S at 128 b, its P at 256 + 64 b, O at 384.
 constexpr int kTmemCols = 512, kTmemP = 256, kTmemO = 384;
 // What beginning and ending a tile (queries, joining, filling and draining) costs,
-// in pages: about 14000 cycles against 1050 a page.
-constexpr int kTileCost = 12;
+// in pages: about 14000 cycles against 900 a page.
+constexpr int kTileCost = 16;
 constexpr int kKStages = 4, kVStages = 3, kFStages = 2;  // steps of k, of v, of v in fp16
 constexpr int kScales = 8;       // steps whose scales are kept: more than a softmax lags behind the producer
 
@@ -381,9 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     }
             }
         } else if (wid == kIssuer || wid == kIssuer + 1) {
-            // ---- MMA issue, one thread for S and one for O (their warps find the
-            // segments).  A block that gave up goes on without waiting, on whatever is there.
-            const bool scores = wid == kIssuer;
+            // ---- MMA issue, a warp for S and one for O, an elected lane of each.  A
+            // block that gave up goes on without waiting, on whatever is there.
+            const bool scores = __shfl_sync(0xffffffffu, wid, 0) == kIssuer;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t qd = desc_lo(smem_u32(qbuf)), kd = desc_lo(smem_u32(kbuf)), fd = desc_lo(smem_u32(fbuf));
             int slot = 0, nseg = 0;      // buffer of the next step; segments so far
             uint32_t phase = 0, n = 0;   // of that buffer; steps so far
@@ -391,42 +392,51 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
                 const int steps = (s.pe - s.p0 + 1) / 2;
                 u += s.units;
-                __syncwarp();
-                if (lane != 0 || s.p1 == 0) continue;
+                if (s.p1 == 0) continue;
                 if (scores) {
                     wait_or_abort(&ct->q_ready, nseg++ & 1, p, &ct->abort);
                     for (int i = 0; i < steps; ++i, ++n) {
-                        const uint32_t b = n & 1, d = tmem + 128 * b, k = kd + slot * (kStep / 16);
+                        const uint32_t b = n & 1, d = tm + 128 * b, k = kd + slot * (kStep / 16);
                         wait_or_abort(&ct->k_full[slot], phase, p, &ct->abort);
                         if (n >= 2) wait_or_abort(&ct->s_read[b], (n / 2 - 1) & 1, p, &ct->abort);
+                        __syncwarp();
                         tc_fence_after();
-                        mma_f8<false>(d, qd, k, desc_hi(D), mma_idesc(kKeys));
+                        if (elect_one()) {
+                            mma_f8<false>(d, qd, k, desc_hi(D), mma_idesc(kKeys));
 #pragma unroll
-                        for (int j = 1; j < D / 32; ++j) mma_f8<true>(d, qd + 2 * j, k + 2 * j, desc_hi(D), mma_idesc(kKeys));
+                            for (int j = 1; j < D / 32; ++j) mma_f8<true>(d, qd + 2 * j, k + 2 * j, desc_hi(D), mma_idesc(kKeys));
 #pragma unroll
-                        for (int j = 0; j < D / 32; ++j)
-                            mma_f8<true>(d, qd + kRows * D / 16 + 2 * j, k + 2 * j, desc_hi(D), mma_idesc(kKeys));
-                        tc_commit(&ct->s_ready[b]);
-                        tc_commit(&ct->k_empty[slot]);
+                            for (int j = 0; j < D / 32; ++j)
+                                mma_f8<true>(d, qd + kRows * D / 16 + 2 * j, k + 2 * j, desc_hi(D), mma_idesc(kKeys));
+                            tc_commit(&ct->s_ready[b]);
+                            tc_commit(&ct->k_empty[slot]);
+                        }
+                        __syncwarp();
                         if (++slot == kKStages) slot = 0, phase ^= 1;
                     }
                 } else {
                     for (int i = 0; i < steps; ++i, ++n) {
-                        const uint32_t b = n & 1, a = tmem + kTmemP + 64 * b, f = fd + slot * (2 * kStep / 16);
+                        const uint32_t b = n & 1, a = tm + kTmemP + 64 * b, f = fd + slot * (2 * kStep / 16);
                         wait_or_abort(&ct->f_full[slot], phase, p, &ct->abort);
                         wait_or_abort(&ct->p_ready[b], (n / 2) & 1, p, &ct->abort);
+                        __syncwarp();
                         tc_fence_after();
+                        const uint32_t add = i > 0;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)  // 16 tokens each: four of each page
-                            mma_f16_ts(tmem + kTmemO, a + 8 * j, f + (j >> 2) * (2 * kPageBytes / 16) + 2 * (j & 3), desc_hi(128),
-                                       mma_idesc(D), j > 0 ? 1 : i > 0);
-                        tc_commit(&ct->o_ready[b]);
-                        tc_commit(&ct->f_empty[slot]);
+                            for (int j = 0; j < 8; ++j)  // 16 tokens each: four of each page
+                                mma_f16_ts(tm + kTmemO, a + 8 * j, f + (j >> 2) * (2 * kPageBytes / 16) + 2 * (j & 3),
+                                           desc_hi(128), mma_idesc(D), j > 0 ? 1 : add);
+                            tc_commit(&ct->o_ready[b]);
+                            tc_commit(&ct->f_empty[slot]);
+                        }
+                        __syncwarp();
                         if (++slot == kFStages) slot = 0, phase ^= 1;
                     }
                 }
+                __syncwarp();
             }
-            if (lane == 0 && aborted()) {
+            if (__any_sync(0xffffffffu, aborted()) && elect_one()) {
                 // no block ends with products in flight
                 tc_commit(&ct->drained[scores]);
                 const uint64_t t0 = gtimer();

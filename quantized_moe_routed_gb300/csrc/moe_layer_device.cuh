@@ -58,6 +58,16 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// One lane of a converged warp, the same every time.  A warp that stays together
+// and elects the lane that issues keeps descriptors and addresses in uniform
+// registers; a branch on the lane's number costs a move a product and operand.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t is;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(is));
+    return is != 0;
+}
+
 // Launch configuration shared by the operators: programmatic dependent launch
 // (every kernel calls grid_wait before its first access).
 struct LaunchCfg {

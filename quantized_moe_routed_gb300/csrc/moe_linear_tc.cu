@@ -107,14 +107,6 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&u)[16])
         : "memory");
 }
 
-// One lane of a converged warp, the same every time.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t is;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(is));
-    return is != 0;
-}
-
 template <int TN>
 __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid_constant__ LinearTcParams tp)
 {
