@@ -56,15 +56,19 @@ moe_status_t moe_norm(const void *x_dev, int x_f32, int64_t x_stride, const void
  *   y[t, n] = ts[n] * sum_k E2M1(q[n, k]) * E4M3(s[n, k/16]) * x[t, k]
  * with NVFP4 weights laid out as an expert's projection in moe_plan_desc, and
  * a tensor scale for each row (fused projections keep theirs).  The weights
- * are used exactly; x is rounded to 11 significant bits relative to the
- * largest of each 128 (fp16 operands after a power-of-two prescale); sums in
- * fp32.  Weight block scales may have their sign set; a NaN code gives NaN.
+ * are used exactly; x enters as fp16 after a power-of-two prescale of its row or
+ * of each 128 of it: exact for elements down to 2^-28 of the largest there, what
+ * is smaller off by at most 2^-38 of that largest; sums in fp32.  Weight block scales may have
+ * their sign set; a NaN code gives NaN.
  *   q_dev uint8 [N, K/2], s_dev uint8 [N, K/16], ts_dev float [N]
  *   x_dev bf16 [T, K], rows x_stride elements apart
  *   y_dev float [T, N] (y_bf16 = 0) or bf16 (1), contiguous, fully written
  *   N >= 1, K a multiple of 32 up to 2^22, T >= 0 (0: a no-op).  Meant for decode
- *   batches: up to 24 tokens read the weights once; more run in groups of 24,
- *   each reading them again (from L2 as far as they fit).
+ *   batches: up to 24 tokens read the weights once; more run in groups of 24 (of
+ *   64 where the weights have many rows, K is a multiple of 256 and s_dev 16-byte
+ *   aligned), each reading them again (from L2 as far as they fit).
+ *   A device-side wait that ran out (bounded as in moe_nvfp4.h) leaves NaN in the
+ *   outputs of its block's rows: this call has no workspace to flag it in.
  * q_dev and x_dev 16-byte aligned, s_dev 2-byte, ts_dev 4-byte, y_dev to its
  * element; x_stride >= K and a multiple of 8. */
 moe_status_t moe_linear(const uint8_t *q_dev, const uint8_t *s_dev, const float *ts_dev, int N, int K,
@@ -162,9 +166,11 @@ moe_status_t moe_kv_append(moe_kv_t kv, const void *q_dev, int64_t q_stride, con
  * aligned, stride a multiple of 8); o bf16 [N, q_heads, head_dim] contiguous, 16-byte aligned.
  * A query that sees no token (kv_len[b] smaller than its new tokens) gets 0.
  * Rows of o outside every sequence are not written.  Products use the 8-bit
- * codes as they are: q enters as the sum of two E4M3 digits (exact for elements
- * down to 2^-10 of the row's largest), the softmax weights as two (relative
- * 2^-9); sums, maxima and the softmax in fp32.  A page id out of range counts
+ * codes' exact values.  With up to 16 rows (a sequence's new tokens x query heads
+ * of a kv head) q enters as fp16 (exact for elements down to 2^-28 of the row's
+ * largest), with more as the sum of two E4M3 digits (exact down to 2^-10 of it);
+ * softmax weights are rounded to fp16 (2^-12 of each, or 2^-31 of the row's
+ * largest if more); sums, maxima and the softmax in fp32.  A page id out of range counts
  * as tokens that nothing sees and is flagged for moe_kv_check. */
 moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, float scale, void *o_dev,
                            const moe_kv_batch *batch, void *ws_dev, void *stream);

@@ -9,9 +9,12 @@
 // and scales of k and of v: the scale needs the largest of all new values of
 // the page, and its growth the page's old codes, so a page and head is the
 // unit that no two blocks share (no atomics, the same bits every run).  Another
-// block per (page, kv head) rotates the head group's queries.  Bytes bound it
-// for prefill chunks; for single tokens the chain of dependent loads (lengths,
-// page id, old scale, codes) does.
+// block per (page, kv head) rotates the head group's queries.  The chain of
+// dependent loads (lengths, page id, old scale, codes) bounds it, for single tokens
+// (24 sequences: 5.0 us) and for chunks (4 x 4096 tokens of 32 + 16 heads of 128:
+// 37.9 us, 54% of the rate of a copy of the same bytes), where 64 registers a thread let
+// two blocks of 512 share an SM; so the new tokens' loads do not wait for the
+// page's id, and v stays packed until it is coded (44.5 us otherwise).
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -67,8 +70,14 @@ __device__ __forceinline__ void load_angles(const KvParams &c, float2 (&cs)[8], 
 {
     if (ROT == kNone || ROT == kOddHalves) return;
     const float2 *t = reinterpret_cast<const float2 *>(c.rope + static_cast<size_t>(pos) * c.rot_dim) + 8 * u;
+    if (ROT == kHalves) {  // eight pairs, or none (load_unit turns none)
+        if (8 * u >= c.rot_dim / 2) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = 8 * u + i < c.rot_dim / 2 ? __ldg(t + i) : make_float2(1.f, 0.f);
+        for (int i = 0; i < 8; ++i) cs[i] = __ldg(t + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = 8 * u + i < c.rot_dim / 2 ? __ldg(t + i) : make_float2(1.f, 0.f);
+    }
 }
 
 // (a, b) turned: every product and sum rounded on its own, so that the values are
@@ -117,6 +126,14 @@ __device__ __forceinline__ void load_unit(const KvParams &c, float (&v)[16], con
             v[i] = d < half ? turn_a(v[i], o, __ldg(t + d)) : turn_b(o, v[i], __ldg(t + d - half));
         }
     }
+}
+
+// The larger of a and b, or NaN where either is one.
+__device__ __forceinline__ float nan_max(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // The block's largest of a and of b.
@@ -201,28 +218,38 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
         }
     }
     const int page0 = max(first, 0) / kPage;
-    for (int pg = page0 + blockIdx.x; pg * kPage < len; pg += gridDim.x) {
-        const int pos0 = max(pg * kPage, first);                        // first new token of the page
-        const int cnt = min(pg * kPage + kPage, len) - pos0;            // new tokens of the page
-        const int row0 = q0 + (pos0 - first);                           // its row in q, k and v
-        const int slot0 = pos0 - pg * kPage;
-        const int id = c.pages[static_cast<size_t>(b) * c.max_pages + pg];
-        const bool ok = id >= 0 && id < c.n_pages && (c.rot_dim == 0 || pos0 + cnt <= c.rope_positions);
-        if (!ok && tid == 0) atomicOr(c.ctrl + 2, kErrBadIndex);
-        if (queries) {
+    struct Page {
+        int pos0, cnt;  // first new token of the page, its new tokens
+        int row0;       // that token's row in q, k and v
+        int slot0, id;  // its slot; the page's id, which the new tokens' loads do not wait for
+        bool turns;     // all positions are inside the table
+    };
+    auto page = [&](int pg) {
+        Page r;
+        r.pos0 = max(pg * kPage, first);
+        r.cnt = min(pg * kPage + kPage, len) - r.pos0;
+        r.row0 = q0 + (r.pos0 - first);
+        r.slot0 = r.pos0 - pg * kPage;
+        r.id = c.pages[static_cast<size_t>(b) * c.max_pages + pg];
+        r.turns = c.rot_dim == 0 || r.pos0 + r.cnt <= c.rope_positions;
+        return r;
+    };
+    // (two loops: in one, what either kind of block needs would be held through the other's)
+    if (queries) {
+        for (int pg = page0 + blockIdx.x; pg * kPage < len; pg += gridDim.x) {
+            const auto [pos0, cnt, row0, slot0, id, turns] = page(pg);
             const int G = c.q_heads / hk;
             if (const int tok = tid / UT, u = tid % UT; tok < cnt) {
                 const Units<ROT> un(c, u);
                 float2 cs[8];
-                if (ok) load_angles<ROT>(c, cs, pos0 + tok, u);
+                if (turns) load_angles<ROT>(c, cs, pos0 + tok, u);
                 const uint16_t *src = p.q + (row0 + tok) * p.q_stride + h * G * D;
                 uint16_t *dst = p.q_out + (static_cast<size_t>(row0 + tok) * c.q_heads + h * G) * D;
-#pragma unroll 2
+#pragma unroll 1
                 for (int g = 0; g < G; ++g) {
                     float v[16];
-                    if (ok) {
-                        load_unit<ROT>(c, v, src + g * D, un, cs, pos0 + tok);
-                    } else {
+                    if (turns) load_unit<ROT>(c, v, src + g * D, un, cs, pos0 + tok);
+                    if (!turns || id < 0 || id >= c.n_pages) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = 0.f;
                     }
@@ -233,42 +260,49 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
                                        pack_bf16(v[8 * y + 4], v[8 * y + 5]), pack_bf16(v[8 * y + 6], v[8 * y + 7]));
                 }
             }
+        }
+        return;
+    }
+    for (int pg = page0 + blockIdx.x; pg * kPage < len; pg += gridDim.x) {
+        const auto [pos0, cnt, row0, slot0, id, turns] = page(pg);
+        const int tok = tid / UT, u = tid % UT;
+        const bool in = tok < cnt;
+        const Units<ROT> un(c, u);
+        float x[16];  // the thread's unit of k
+        uint4 z[2];   // and of v, as it is
+        if (in && turns) {
+            float2 cs[8];
+            const uint4 *zp = reinterpret_cast<const uint4 *>(p.v + (row0 + tok) * p.v_stride + h * D + 16 * u);
+            z[0] = zp[0];
+            z[1] = zp[1];
+            load_angles<ROT>(c, cs, pos0 + tok, u);
+            load_unit<ROT>(c, x, p.k + (row0 + tok) * p.k_stride + h * D, un, cs, pos0 + tok);
+        }
+        if (!turns || id < 0 || id >= c.n_pages) {
+            if (tid == 0) atomicOr(c.ctrl + 2, kErrBadIndex);
             continue;
         }
-        if (!ok) continue;
         const size_t ph = static_cast<size_t>(id) * hk + h;
         const float old_ks = c.ks[ph], old_vs = c.vs[ph];
         __syncthreads();  // the last page's readers of shared memory are done
         if (tid < kPage) bad_tok[tid] = 0;
         __syncthreads();
-        const int tok = tid / UT, u = tid % UT;
-        const bool in = tok < cnt;
-        const Units<ROT> un(c, u);
-        float x[16], z[16];  // the thread's unit of k and of v
-        if (in) {
-            float2 cs[8];
-            load_angles<ROT>(c, cs, pos0 + tok, u);
-            load_unit<ROT>(c, x, p.k + (row0 + tok) * p.k_stride + h * D, un, cs, pos0 + tok);
-            load_unit<kNone>(c, z, p.v + (row0 + tok) * p.v_stride + h * D, Units<kNone>(c, u), cs, pos0 + tok);
-            bool bad = false;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) bad |= !(fabsf(x[j]) <= kMaxValue) || !(fabsf(z[j]) <= kMaxValue);
-            if (bad) bad_tok[tok] = 1;
-        }
-        __syncthreads();
         float ak = 0.f, av = 0.f;
         if (in) {
-            const bool bad = bad_tok[tok] != 0;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (bad) {
-                    x[j] = __int_as_float(0x7FC00000);
-                    z[j] = 0.f;
-                } else {
-                    ak = fmaxf(ak, fabsf(x[j]));
-                    av = fmaxf(av, fabsf(z[j]));
-                }
-            }
+            for (int j = 0; j < 16; ++j) ak = nan_max(ak, fabsf(x[j]));
+            uint32_t am = 0u;  // v's largest magnitude, as bits (a NaN's are above infinity's)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) am = __vmaxu2(am, u4w(z[j >> 2], j & 3) & 0x7FFF7FFFu);
+            av = __uint_as_float(max(am >> 16, am & 0xFFFFu) << 16);
+            if (!(ak <= kMaxValue) || !(av <= kMaxValue)) bad_tok[tok] = 1;
+        }
+        __syncthreads();
+        if (in && bad_tok[tok] != 0) {
+            ak = av = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = __int_as_float(0x7FC00000);
+            z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
         }
         block_max2<kThreads>(ak, av, red);
         float fk, fv;
@@ -287,7 +321,8 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
             uint8_t *t = reinterpret_cast<uint8_t *>(vt) + 16 * u * kStride + slot0 + tok;
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
-                const uint32_t w = e4m3_pack4(z[j] * iv, z[j + 1] * iv, z[j + 2] * iv, z[j + 3] * iv);
+                const uint32_t z0 = u4w(z[j >> 3], (j >> 1) & 3), z1 = u4w(z[j >> 3], ((j >> 1) & 3) + 1);
+                const uint32_t w = e4m3_pack4(bf16_lo(z0) * iv, bf16_hi(z0) * iv, bf16_lo(z1) * iv, bf16_hi(z1) * iv);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) t[(j + b) * kStride] = static_cast<uint8_t>(w >> (8 * b));
             }

@@ -168,7 +168,7 @@ moe_status_t moe_norm(const void *x_dev, int x_f32, int64_t x_stride, const void
     const moe::NormParams p{x_dev, x_stride, static_cast<const uint16_t *>(r_dev), static_cast<uint16_t *>(r_out_dev),
                             static_cast<const uint16_t *>(w_dev), static_cast<uint16_t *>(y_dev), q_dev, q_scale_dev,
                             eps, T, H, x_f32};
-    return launched(moe::launch_norm(p, dev.sms, static_cast<cudaStream_t>(stream)), "norm launch");
+    return launched(moe::launch_norm(p, static_cast<cudaStream_t>(stream)), "norm launch");
 }
 
 moe_status_t moe_linear(const uint8_t *q_dev, const uint8_t *s_dev, const float *ts_dev, int N, int K,

@@ -23,7 +23,7 @@ struct NormParams {
     float eps;
     int T, H, x_f32;
 };
-cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_norm(const NormParams &p, cudaStream_t st);
 
 // moe_linear.cu
 struct LinearParams {
