@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                             if (32 * (h & 1) + j >= (h < 2 ? lim0 : lim1)) a[h][j] = -INFINITY;
                 }
                 // the largest, in log2 units (a row's factor is not negative)
-                float fs[2] = {qs * ks.x, qs * ks.y};
+                float fs[2] = {qs * fmaxf(ks.x, 0.f), qs * fmaxf(ks.y, 0.f)};  // (no such page: 0)
                 float mx = -INFINITY;
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
