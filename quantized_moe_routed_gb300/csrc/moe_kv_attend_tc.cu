@@ -27,8 +27,8 @@
 // scores of a warpgroup's next step are computed once it has read this one's,
 // and P V during the following softmax.  Only the reference goes from step to step, as
 // soon as a step's maxima are known.  Two threads bring pages, a warp issues the
-// products for S and one those for O, a warpgroup converts v.  2048 new tokens after
-// 14336, 32 heads of 128 on 8: 456 us, 1280 TFLOP/s; a step takes 1950 cycles, of which
+// products for S and one those for O, two pairs of warps convert v.  2048 new tokens after
+// 14336, 32 heads of 128 on 8: 450 us, 1300 TFLOP/s; a step takes 1920 cycles, of which
 // the tensor cores work 1024 and the exponentials 1024 a pair of warps; the rest are
 // waits between them.  (Commits for each page of P, turns for the exponentials and
 // four softmax warpgroups all measured slower: 484, 537 and 524 us.)  With two row
@@ -66,7 +66,7 @@ constexpr int kTmemCols = 512, kTmemP = 256, kTmemO = 384;
 // What beginning and ending a tile (queries, joining, filling and draining) costs,
 // in pages: about 14000 cycles against 900 a page.
 constexpr int kTileCost = 16;
-constexpr int kKStages = 4, kVStages = 3, kFStages = 2;  // steps of k, of v, of v in fp16
+constexpr int kKStages = 3, kVStages = 4, kFStages = 2;  // steps of k, of v, of v in fp16
 constexpr int kScales = 8;       // steps whose scales are kept: more than a softmax lags behind the producer
 
 struct Control {
@@ -254,10 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&ct->v_full[i], 1);
-            mbar_init(&ct->v_empty[i], 128);
+            mbar_init(&ct->v_empty[i], 64);
         }
         for (int i = 0; i < kFStages; ++i) {
-            mbar_init(&ct->f_full[i], 128);
+            mbar_init(&ct->f_full[i], 64);
             mbar_init(&ct->f_empty[i], 1);
         }
         for (int i = 0; i < kScales; ++i) mbar_init(&ct->sc_full[i], 1);
@@ -291,13 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     if (wid < kSoftmax) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (wid >= kConverter) {
-            // ---- v's codes to fp16: rows of a head dim, 64 tokens of a page (128 bytes)
-            const int t = tid - 32 * kConverter;
+            // ---- v's codes to fp16: rows of a head dim, 64 tokens of a page (128 bytes).
+            // Two warps a step, in turn (an even number of stages: each is always the same pair's).
+            const int t = (tid - 32 * kConverter) & 63, half = (wid - kConverter) >> 1;
             int it = 0;
             for (long long u = u0; u < u1;) {
                 const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
                 const int end = it + (s.pe - s.p0 + 1) / 2;
-                for (; it < end; ++it) {
+                for (it += (it & 1) ^ half; it < end; it += 2) {
                     const int vs = it % kVStages, f = it % kFStages;
                     wait_or_abort(&ct->v_full[vs], (it / kVStages) & 1, p, &ct->abort);
                     if (it >= kFStages) wait_or_abort(&ct->f_empty[f], (it / kFStages - 1) & 1, p, &ct->abort);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     const uint8_t *src = vbuf + vs * kStep;
                     uint8_t *dst = fbuf + f * 2 * kStep;
 #pragma unroll 4
-                    for (int i = t; i < kStep / 16; i += 128) {  // 16 codes: granule i % 4 of row i / 4
+                    for (int i = t; i < kStep / 16; i += 64) {  // 16 codes: granule i % 4 of row i / 4
                         const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 16);
                         uint32_t h[8];
 #pragma unroll
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     mbar_arrive(&ct->f_full[f]);
                     mbar_arrive(&ct->v_empty[vs]);
                 }
+                it = end;
                 u += s.units;
             }
         } else if (wid < kIssuer) {
