@@ -176,7 +176,8 @@ moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, flo
                            const moe_kv_batch *batch, void *ws_dev, void *stream);
 
 /* Synchronise `stream`, read and clear the workspace's error word: MOE_OK,
- * MOE_ERR_TIMEOUT, MOE_ERR_BAD_INDEX, or MOE_ERR_CUDA. */
+ * MOE_ERR_TIMEOUT (initialise the workspace again), MOE_ERR_BAD_INDEX, or
+ * MOE_ERR_CUDA. */
 moe_status_t moe_kv_check(moe_kv_t kv, void *ws_dev, void *stream);
 
 #ifdef __cplusplus
