@@ -28,10 +28,11 @@
 // and P V during the following softmax.  Only the reference goes from step to step, as
 // soon as a step's maxima are known.  Two threads bring pages, a warp issues the
 // products for S and one those for O, two pairs of warps convert v.  2048 new tokens after
-// 14336, 32 heads of 128 on 8: 450 us, 1300 TFLOP/s; a step takes 1920 cycles, of which
+// 14336, 32 heads of 128 on 8: 449 us, 1300 TFLOP/s; a step takes 1920 cycles, of which
 // the tensor cores work 1024 and the exponentials 1024 a pair of warps; the rest are
-// waits between them.  (Commits for each page of P, turns for the exponentials and
-// four softmax warpgroups all measured slower: 484, 537 and 524 us.)  With two row
+// waits between them.  (Commits for each page of P, turns for the exponentials,
+// four softmax warpgroups, an eighth of the exponentials as polynomials all measured
+// slower: 484, 537, 524 and 476 us.)  With two row
 // tiles a block sharing k and v, tensor memory leaves no room for this (S and P in one
 // place): the softmax then waits for the chain from its weights over P V to the next
 // scores, 580 us for 2048 x 16384 tokens and 32 heads.
