@@ -22,6 +22,9 @@
 // element and undone at the end: bf16's 8 bits are exact down to 2^-31 of the
 // token's largest, and what is smaller is off by at most 2^-39 of that largest.
 //
+// Sums are fp32 in tensor memory, a step of 16 elements after another: at K = 4096
+// the result's norm is off by 1e-6, against 1e-7 for mma.sync's shorter runs.
+//
 // A wait that runs out (bounded as everywhere) leaves NaN in the block's rows.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
