@@ -536,6 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 if (move) ref = mx;
                 ct->ref[w][row] = ref;
                 mbar_arrive(&ct->ref_ready[w]);
+                if (i > 1) {
+                    // the last weights in this warpgroup's place have been used.  (Before the
+                    // rescaling too: the other warpgroup's barrier is then at most one
+                    // phase behind the one waited for there, which is all a parity can tell.)
+                    wait_or_abort(&ct->o_ready[w], ph ^ 1, p, &ct->abort);
+                    __syncwarp();
+                    tc_fence_after();
+                }
                 if (__any_sync(0xffffffffu, move) && i > 0) {
                     // the accumulators follow, between the last step's product and this one's
                     wait_or_abort(&ct->o_ready[w ^ 1], ((k - 1) >> 1) & 1, p, &ct->abort);
@@ -556,11 +564,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 const float base = ref == -INFINITY ? 0.f : ref;
                 if (lref != ref) l *= ex2(lref - base);  // (lref = -inf: 0, as l is)
                 lref = ref;
-                if (i > 1) {  // the last weights in this warpgroup's place have been used
-                    wait_or_abort(&ct->o_ready[w], ph ^ 1, p, &ct->abort);
-                    __syncwarp();
-                    tc_fence_after();
-                }
                 // 64 w vs in fp16; w's sum from the unrounded values
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {

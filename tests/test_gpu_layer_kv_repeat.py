@@ -4,8 +4,9 @@ nothing to wait for, and its warps run ahead of each other as far as they can)."
 import pytest
 import torch
 
-from quantized_moe_routed_gb300 import binding
-from test_gpu_layer_kv import Step, _cache, _check_attend, _pool
+import layer_reference as ref
+from quantized_moe_routed_gb300 import KVCache, binding
+from test_gpu_layer_kv import Step, _cache, _check_attend, _gather, _pool
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -90,3 +91,30 @@ def test_bad_pages_count_as_tokens_that_nothing_sees(n, Hq, D):
     rest = Step([n], [700 - 64 * len(bad)], seed=n)
     rest.pages = step.pages[:, [i for i in range(step.pages.shape[1]) if i not in bad]]
     _check_attend(rest, bufs, q, out, D ** -0.5)
+
+
+@pytest.mark.parametrize("gain", [1, 3, 5])
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(16, 64, 8, 128), (16, 64, 8, 64), (200, 16, 4, 128), (1, 64, 8, 128)])
+def test_rows_whose_maximum_moves_now_and_then(n, Hq, Hkv, D, gain):
+    """Long sequences and scores of several units: some row's running maximum moves
+    far, and its accumulators are rescaled between products that are in flight."""
+    L = [16400, 9488, 2576, 12048, 5136, 14608, 7696, 784]
+    for seed in range(6):
+        step = Step([n] * len(L), L, seed=seed)
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        k, v = ((torch.randn(s, generator=g, device=DEV) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                for s in ((step.n_pages, Hkv, 64, D), (step.n_pages, Hkv, D, 64)))
+        sc = torch.full((step.n_pages, Hkv), 2.0 ** -6, device=DEV)
+        cache = KVCache(step.n_pages, Hq, Hkv, D, buffers=dict(k=k, v=v, k_scale=sc, v_scale=sc.clone()))
+        q = (torch.randn((step.N, Hq, D), generator=g, device=DEV) * gain).bfloat16()
+        ws = cache.new_workspace()
+        args = (*step.dev(), ws, n)
+        first = cache.attend(q, *args)
+        assert sum(not torch.equal(cache.attend(q, *args), first) for _ in range(100)) == 0
+        assert cache.check(ws) == 0
+        # one sequence and kv head against the definition
+        b, h, G = 7, Hkv - 1, Hq // Hkv
+        kk, vv = _gather(step, [t.cpu() for t in (k, v, sc, sc)], b, h)
+        got = first[b * n:(b + 1) * n, h * G:].cpu().double()
+        want = ref.attend(q[b * n:(b + 1) * n, h * G:].cpu(), kk, vv, n, L[b], D ** -0.5)[0]
+        assert float((got - want).norm() / want.norm()) < 2 ** -6
