@@ -65,7 +65,7 @@ moe_status_t moe_norm(const void *x_dev, int x_f32, int64_t x_stride, const void
  *   y_dev float [T, N] (y_bf16 = 0) or bf16 (1), contiguous, fully written
  *   N >= 1, K a multiple of 32 up to 2^22, T >= 0 (0: a no-op).  Meant for decode
  *   batches: up to 24 tokens read the weights once; more run in groups of 24 (of
- *   64 where the weights have many rows, K is a multiple of 256 and s_dev 16-byte
+ *   32 where the weights have many rows, K is a multiple of 256 and s_dev 16-byte
  *   aligned), each reading them again (from L2 as far as they fit).
  *   A device-side wait that ran out (bounded as in moe_nvfp4.h) leaves NaN in the
  *   outputs of its block's rows: this call has no workspace to flag it in.

@@ -127,9 +127,9 @@ int attend_tile_rows(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 :
 // Whether the tensor-core kernel takes a product: where its loads may go, and where
 // the rows and the length give it enough work past what it takes to begin (every
 // block reads all of x first).  Measured, it against the others, at K = 4096: 8
-// tokens, 64 rows an SM 14.7 / 12.4 us, 96 rows 14.9 / 16.5, 512 rows 37 / 44; 24
-// tokens, 64 rows 20.2 / 20.2, 128 rows 21 / 28, 512 rows 43 / 76; 64 tokens, 64
-// rows 41 / 55.  At K = 1024: 8 tokens, 128 rows 9.1 / 7.5, 256 rows 10.5 / 10.3;
+// tokens, 64 rows an SM 14.7 / 12.4 us, 96 rows 15.6 / 16.5, 512 rows 41 / 44; 24
+// tokens, 64 rows 20.6 / 20.2, 128 rows 21 / 28, 512 rows 47 / 76; 64 tokens, 64
+// rows 47 / 55.  At K = 1024: 8 tokens, 128 rows 9.1 / 7.5, 256 rows 10.5 / 10.3;
 // 24 tokens, 128 rows 10.4 / 10.7.
 bool linear_on_tensor_cores(const moe::LinearParams &p, int sms)
 {

@@ -8,11 +8,11 @@
 // warpgroups, a thread a row, turn them into fp16 (E2M1 times E4M3 is exact there)
 // and store them to tensor memory as the A operand of tcgen05.mma (shared memory
 // would have to take and give each of those bytes, at four times the weights' own);
-// tokens are the N axis (16, 32 or 64), staged in shared memory as fp16.  The tiles
+// tokens are the N axis (16 or 32), staged in shared memory as fp16.  The tiles
 // take a piece of K in turn, so x passes by once.  The rows of a tile are the
 // block's rows over its tiles, not 128: every block brings the same number of bytes.
 //
-// 24 tokens, 65543 rows of 4096: 40.6 us, 57% of the rate at which memory could
+// 24 tokens, 65543 rows of 4096: 44.7 us, 52% of the rate at which memory could
 // bring the weights (66 us with mma.sync).  The conversion bounds it (two
 // instructions per pair of weights, 8 warps), then the pass over x that finds the
 // tokens' scales (every block reads all of x before its first product, 5 us) and the
@@ -22,8 +22,9 @@
 // element and undone at the end: bf16's 8 bits are exact down to 2^-31 of the
 // token's largest, and what is smaller is off by at most 2^-39 of that largest.
 //
-// Sums are fp32 in tensor memory, a step of 16 elements after another: at K = 4096
-// the result's norm is off by 1e-6, against 1e-7 for mma.sync's shorter runs.
+// Sums on the tensor cores run over 512 elements of K, then go on in fp32 additions
+// that round, in tensor memory beside them: 1.1e-7 of the result's norm at K = 4096,
+// as with mma.sync; in one run over all of K, 1e-6 (and 40.4 us).
 //
 // A wait that runs out (bounded as everywhere) leaves NaN in the block's rows.
 #include "moe_internal.h"
@@ -49,24 +50,25 @@ constexpr int kThreads = 512;
 // first warps of each kind
 constexpr int kProducer = 0, kIssuer = 1, kStager = 4, kConverter = 8;  // (two issuers)
 constexpr int kTmemCols = 512;
-constexpr int kMaxStages = 10;
+// Pieces of a tile whose products are added up on the tensor cores before the sum
+// goes on in fp32 additions that round: a long run there loses a digit.
+constexpr int kRun = 2;
 
 // Buffers of A in tensor memory (128 elements of K, 64 columns each) that a
-// converting warpgroup has: the columns that the accumulators leave.
+// converting warpgroup has: the columns that accumulators and sums leave.
 template <int TN>
-__host__ __device__ constexpr int buffers() { return (kTmemCols - kTiles * TN) / 64 / 2; }
+__host__ __device__ constexpr int buffers() { return (kTmemCols - 2 * kTiles * TN) / 64 / 2; }
 // Stages of weights: an even number, so that a stage always belongs to the same
 // warpgroup (a barrier's parity tells neighbouring phases apart, no more).
-template <int TN>
-__host__ __device__ constexpr int stages() { return TN == 64 ? 8 : 10; }
+constexpr int kStages = 10;
 
 struct Control {
-    alignas(16) float scale[64], back[64];  // each token's power of two and its inverse
-    uint64_t full[kMaxStages], empty[kMaxStages];
+    alignas(16) float scale[32], back[32];  // each token's power of two and its inverse
+    uint64_t full[kStages], empty[kStages];
     uint64_t x_full[2], x_empty[2];
     uint64_t a_full[2][3], a_empty[2][3];
     uint64_t d_ready, drained[2];
-    uint32_t amax[64];          // largest magnitude of each token, as bits
+    uint32_t amax[32];          // largest magnitude of each token, as bits
     uint32_t tmem;
     int abort;
 };
@@ -113,7 +115,7 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&u)[16])
 template <int TN>
 __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid_constant__ LinearTcParams tp)
 {
-    constexpr int NS = stages<TN>(), NB = buffers<TN>();
+    constexpr int NS = kStages, NB = buffers<TN>();
     constexpr int kX = TN * kPiece * 2;  // bytes of a piece of x: four blocks of 64 elements, TN rows of 128 bytes
     extern __shared__ uint8_t smem_raw[];
     uint8_t *codes = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
                     __syncwarp();
                     tc_fence_after();
                     const uint32_t a = tm + kTmemCols - 2 * NB * 64 + (w * NB + b) * 64, x = xd + ((k & 1) * kX + half * (kX / 2)) / 16;
-                    const uint32_t add = half > 0 || (it > 1 && k > 0);
+                    const uint32_t add = half > 0 || (tiles == 1 ? k >> 1 : k) % kRun != 0;
                     if (elect_one()) {
                         mma_f16_ts(d, a, x, idesc, add);
 #pragma unroll
@@ -312,6 +314,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
             return r;
         };
         uint4 s1st = load_scales(), s2nd = load_scales();
+        // a tile's sum so far: from the accumulator, which the next run starts over, to
+        // columns of its own.  The tile's last stage was this warpgroup's last or, with four
+        // tiles, the one before; its products are done when its last buffer is free.
+        Place now{w / tiles, w % tiles};
+        auto keep_sum = [&](int slot, bool more) {
+            const int last = used - (tiles == kTiles ? 3 : 1);
+            if (last + NB >= used) wait(&ct->a_empty[w][last % NB], (last / NB) & 1);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < TN; c += 16) {
+                const uint32_t at = tmem + lanes + slot * TN + c;
+                float v[16], u[16];
+                uint32_t x[16];
+                tc_ld16(at, v);
+                if (more) tc_ld16(at + kTiles * TN, u);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(more ? v[j] + u[j] : v[j]);
+                tc_st16(at + kTiles * TN, x);
+            }
+            tc_wait_st();
+        };
         int st = w;
         uint32_t round = 0;
         for (int it = w; it < total; it += 2) {
@@ -319,6 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
             const uint4 s16 = s1st;
             s1st = s2nd;
             s2nd = load_scales();
+            if (const int run = tiles == 1 ? now.k >> 1 : now.k; run > 0 && run % kRun == 0)
+                keep_sum(tiles == 1 ? w : now.m, run > kRun);
+            now.next(tiles);
             wait(&ct->full[st], round);
             uint4 q[8];
 #pragma unroll
@@ -369,6 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
         tc_fence_after();
         const float nan = __int_as_float(0x7FC00000);
         const bool poison = aborted(), two = tiles == 1 && pieces > 1;  // two: one tile, each warpgroup's half of K apart
+        // sums kept beside the accumulators
+        const bool sums = (tiles == 1 ? (pieces + 1) / 2 : pieces) > kRun, sums2 = pieces / 2 > kRun;
 #pragma unroll
         for (int i = 0; i < kTiles / 2; ++i) {
             const int m = w + 2 * i, n = row0 + m * tp.rows + row;
@@ -378,15 +408,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
             size_t o = tok0 * N + n;
 #pragma unroll 1
             for (int c = 0; c < T; c += 4, o += 4 * N) {
-                float4 v, u = make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 v, u[3] = {};
                 __syncwarp();
                 tc_ld4(tmem + lanes + m * TN + c, v);
-                if (two) tc_ld4(tmem + lanes + TN + c, u);
+                if (sums) tc_ld4(tmem + lanes + (kTiles + m) * TN + c, u[0]);
+                if (two) tc_ld4(tmem + lanes + TN + c, u[1]);
+                if (two && sums2) tc_ld4(tmem + lanes + (kTiles + 1) * TN + c, u[2]);
                 tc_wait_ld();
                 if (!in) continue;
                 const float4 f = *reinterpret_cast<const float4 *>(&ct->back[c]);
-                const float y[4] = {(v.x + u.x) * f.x * ts[i], (v.y + u.y) * f.y * ts[i], (v.z + u.z) * f.z * ts[i],
-                                    (v.w + u.w) * f.w * ts[i]};
+                v = f4add(f4add(v, u[0]), f4add(u[1], u[2]));
+                const float y[4] = {v.x * f.x * ts[i], v.y * f.y * ts[i], v.z * f.z * ts[i], v.w * f.w * ts[i]};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (c + j >= T) break;
@@ -408,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
 template <int TN>
 cudaError_t launch_tn(const LinearTcParams &p, int blocks, cudaStream_t st)
 {
-    constexpr int smem = 1024 + stages<TN>() * kCodes + 2 * TN * kPiece * 2 + static_cast<int>(sizeof(Control));
+    constexpr int smem = 1024 + kStages * kCodes + 2 * TN * kPiece * 2 + static_cast<int>(sizeof(Control));
     static_assert(smem <= 227 * 1024, "shared memory of a block");
     static_assert(buffers<TN>() <= 3, "barriers of the buffers of A");
     auto *fn = moe_linear_tc_kernel<TN>;
@@ -434,7 +466,7 @@ LinearTcPlan linear_tc_plan(const LinearParams &p, int num_sms)
 
 cudaError_t launch_linear_tc(const LinearTcParams &p, int blocks, cudaStream_t st)
 {
-    return p.l.T <= 16 ? launch_tn<16>(p, blocks, st) : (p.l.T <= 32 ? launch_tn<32>(p, blocks, st) : launch_tn<64>(p, blocks, st));
+    return p.l.T <= 16 ? launch_tn<16>(p, blocks, st) : launch_tn<32>(p, blocks, st);
 }
 
 }  // namespace moe
