@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
                 const int steps = (s.pe - s.p0 + 1) / 2;
                 u += s.units;
-                if (s.p1 == 0) continue;
+                if (steps == 0) continue;  // (the softmax warps bring no queries then)
                 if (scores) {
                     wait_or_abort(&ct->q_ready, nseg++ & 1, p, &ct->abort);
                     for (int i = 0; i < steps; ++i, ++n) {
@@ -467,21 +467,25 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const int steps = (s.pe - s.p0 + 1) / 2;
             __syncwarp();
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last segment is over
-            {
+            // Queries only where there are steps: the barrier's phase for them is then one that the
+            // scores' issuer has passed before the segment ends.  A segment without
+            // steps waits for nothing of the issuer's, so two of them in a row could
+            // complete two phases between two of its polls, which a parity cannot tell from none.
+            if (steps > 0) {
                 const int qr = ctid >> 1, r = row0 + qr;
                 const float f = put_query<D>(qbuf, qr, ctid & 1,
                                              p.q + static_cast<long long>(q0 + r / G) * p.q_stride + (s.h * G + r % G) * D,
                                              r < rows, p.scale_log2);
                 if ((ctid & 1) == 0) ct->qs[qr] = f;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_fence_before();
+                mbar_arrive(&ct->q_ready);
+                __syncwarp();
+                asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc_fence_before();
-            mbar_arrive(&ct->q_ready);
-            __syncwarp();
-            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             const int r = row0 + row;
             const int sees = r < rows ? row_sees(len, n, G, r) : 0;
-            const float qs = sees > 0 ? ct->qs[row] : 0.f;
+            const float qs = steps > 0 && sees > 0 ? ct->qs[row] : 0.f;
             const int tile_sees = row_sees(len, n, G, row0);  // the least of the tile's rows
 
             float l = 0.f, lref = -INFINITY;  // this warpgroup's sum and what it refers to
