@@ -21,7 +21,7 @@ SOURCES = ("moe_kernels.cu", "moe_tc.cu", "moe_small.cu", "moe_gemv.cu", "moe_ro
            "moe_norm.cu", "moe_linear.cu", "moe_linear_tc.cu", "moe_kv_append.cu", "moe_kv_attend.cu", "moe_kv_attend_tc.cu",
            "moe_layer.cu")
 HEADERS = ("moe_internal.h", "moe_device.cuh", "moe_tcgen05.cuh", "moe_host.h", "moe_layer_internal.h",
-           "moe_layer_device.cuh", "moe_attend.cuh")
+           "moe_layer_device.cuh", "moe_attend.cuh", "moe_ring.h")
 ABI = ("moe_nvfp4.h", "moe_layer.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -28,6 +28,7 @@
 // two to a bank.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
+#include "moe_ring.h"
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -61,6 +62,7 @@ constexpr int kGroups = kWarps / kPageWarps;
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
     float ks[kMaxStages], vs[kMaxStages];  // scales of the stage's page; ks < 0: no such page
+    int issued[4];  // by a producer warp: one past its last page
     int abort, last;
 };
 
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
         // odd pages (one thread's issue alone would bound the kernel)
         const bool values = wid & 1;
         const int odd = (wid - kWarps) >> 1;
-        int it = 0;
+        int it = 0, issued = 0;
         const uint64_t pol = policy_evict_first();
         for (long long u = u0; u < u1;) {
             const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                                 else
                                     tma2d(dst, &c.tm_k, 0, static_cast<int>(ph * kPage), &ct->full[st], pol);
                             }
+                            issued = n + 1;
                         }
                     }
                     __syncwarp();
@@ -150,235 +153,243 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
             }
             u += s.units;
         }
-        // every copy is waited for by the warp that uses it, unless it gave up:
-        // no block ends with a copy into its shared memory in flight
-        if (lane == 0 && *reinterpret_cast<volatile int *>(&ct->abort)) {
-            const uint64_t t0 = gtimer();
-            for (int j = max(it - NS, 0); j < it; ++j)
-                while (!mbar_test(&ct->full[j % NS], (j / NS) & 1) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
+        if (lane == 0) ct->issued[wid - kWarps] = issued;
+    } else {
+        // ---- consumers
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+        int it0 = 0;  // pages of this block before the segment
+        for (long long u = u0; u < u1;) {
+            const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
+            u += s.units;
+            if (s.p1 == 0) continue;
+            const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b];
+
+            // q: fp16 of the lane's D / 4 elements of rows g and g + 8 of the tile
+            uint32_t qf[2][2 * KS];
+            float qs[NX];
+            int sees[NX];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = s.tile * TR + 8 * x + g;
+                const bool in = x < NX && r < rows;
+                uint4 w[KS / 2];
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<long long>(q0 + r / G) * p.q_stride +
+                                                                   (s.h * G + r % G) * D + (D / 4) * t4);
+#pragma unroll
+                for (int i = 0; i < KS / 2; ++i) w[i] = in ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+                if (x < NX) {
+                    uint32_t am = 0u;  // largest magnitude, as bits (16-bit halves)
+#pragma unroll
+                    for (int i = 0; i < 2 * KS; ++i) am = __vmaxu2(am, u4w(w[i >> 2], i & 3) & 0x7FFF7FFFu);
+                    am = max(am >> 16, am & 0xFFFFu);
+                    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+                    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+                    const int e = max(-120, min(120, f16_prescale_exp(__uint_as_float(am << 16))));
+                    const float f = exp2i(e);
+#pragma unroll
+                    for (int i = 0; i < 2 * KS; ++i) qf[x][i] = bf16x2_to_f16x2_scaled(u4w(w[i >> 2], i & 3), f);
+                    // a NaN or an infinity in the row: NaN scores
+                    qs[x < NX ? x : 0] = am >= 0x7F80u ? __int_as_float(0x7FC00000) : exp2i(-e) * p.scale_log2;
+                    sees[x < NX ? x : 0] = in ? row_sees(len, n, G, r) : 0;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * KS; ++i) qf[x][i] = 0u;
                 }
-        }
-        return;
-    }
-
-    // ---- consumers
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
-    int it0 = 0;  // pages of this block before the segment
-    for (long long u = u0; u < u1;) {
-        const Segment s = locate<kTileCost>(sq, c.B, G, TR, u, u1);
-        u += s.units;
-        if (s.p1 == 0) continue;
-        const int n = sq.n[s.b], len = sq.len[s.b], rows = n * G, q0 = sq.q0[s.b];
-
-        // q: fp16 of the lane's D / 4 elements of rows g and g + 8 of the tile
-        uint32_t qf[2][2 * KS];
-        float qs[NX];
-        int sees[NX];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = s.tile * TR + 8 * x + g;
-            const bool in = x < NX && r < rows;
-            uint4 w[KS / 2];
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<long long>(q0 + r / G) * p.q_stride +
-                                                               (s.h * G + r % G) * D + (D / 4) * t4);
-#pragma unroll
-            for (int i = 0; i < KS / 2; ++i) w[i] = in ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-            if (x < NX) {
-                uint32_t am = 0u;  // largest magnitude, as bits (16-bit halves)
-#pragma unroll
-                for (int i = 0; i < 2 * KS; ++i) am = __vmaxu2(am, u4w(w[i >> 2], i & 3) & 0x7FFF7FFFu);
-                am = max(am >> 16, am & 0xFFFFu);
-                am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-                am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-                const int e = max(-120, min(120, f16_prescale_exp(__uint_as_float(am << 16))));
-                const float f = exp2i(e);
-#pragma unroll
-                for (int i = 0; i < 2 * KS; ++i) qf[x][i] = bf16x2_to_f16x2_scaled(u4w(w[i >> 2], i & 3), f);
-                // a NaN or an infinity in the row: NaN scores
-                qs[x < NX ? x : 0] = am >= 0x7F80u ? __int_as_float(0x7FC00000) : exp2i(-e) * p.scale_log2;
-                sees[x < NX ? x : 0] = in ? row_sees(len, n, G, r) : 0;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * KS; ++i) qf[x][i] = 0u;
             }
-        }
-        const int tile_sees = row_sees(len, n, G, s.tile * TR);  // the tile's first row sees the least
+            const int tile_sees = row_sees(len, n, G, s.tile * TR);  // the tile's first row sees the least
 
-        float m[NX], l[NX];
+            float m[NX], l[NX];
 #pragma unroll
-        for (int x = 0; x < NX; ++x) {
-            m[x] = -INFINITY;
-            l[x] = 0.f;
-        }
-        float o[DT][4];
+            for (int x = 0; x < NX; ++x) {
+                m[x] = -INFINITY;
+                l[x] = 0.f;
+            }
+            float o[DT][4];
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+            for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+                for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
-        const int half = wid % kPageWarps;
-        for (int pg = s.p0 + (wid / kPageWarps + kGroups - it0 % kGroups) % kGroups; pg < s.pe; pg += kGroups) {
-            const int it = it0 + pg - s.p0, st = it % NS;
-            wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);
-            __syncwarp();
-            const uint8_t *kp = smem + st * kStage, *vp = kp + kPage * D;
-            const float ks = ct->ks[st], vs = ct->vs[st];
-            if (ks < 0.f) {  // no such page: nothing sees its tokens
+            const int half = wid % kPageWarps;
+            for (int pg = s.p0 + (wid / kPageWarps + kGroups - it0 % kGroups) % kGroups; pg < s.pe; pg += kGroups) {
+                const int it = it0 + pg - s.p0, st = it % NS;
+                wait_or_abort(&ct->full[st], (it / NS) & 1, p, &ct->abort);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ct->empty[st]);
-                continue;
-            }
-            // scores: K step by K step over independent accumulators
-            float sc[NJ][4];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
-#pragma unroll
-            for (int i = 0; i < KS / 4; ++i) {
-                uint4 w[NJ];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const int tok = 16 * (g >> 1) + 2 * (NJ * half + j) + (g & 1);
-                    const int gr = D == 128 ? ((2 * t4 + i) ^ (tok & 7)) : t4;
-                    w[j] = *reinterpret_cast<const uint4 *>(kp + tok * D + gr * 16);
+                const uint8_t *kp = smem + st * kStage, *vp = kp + kPage * D;
+                const float ks = ct->ks[st], vs = ct->vs[st];
+                if (ks < 0.f) {  // no such page: nothing sees its tokens
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ct->empty[st]);
+                    continue;
                 }
+                // scores: K step by K step over independent accumulators
+                float sc[NJ][4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int a = 2 * (4 * i + y);
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
+#pragma unroll
+                for (int i = 0; i < KS / 4; ++i) {
+                    uint4 w[NJ];
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) {
-                        const uint32_t k4 = u4w(w[j], y);
-                        mma16816(sc[j], qf[0][a], qf[1][a], qf[0][a + 1], qf[1][a + 1],
-                                 e4m3x2_to_f16x2(static_cast<uint16_t>(k4)), e4m3x2_to_f16x2(static_cast<uint16_t>(k4 >> 16)));
+                        const int tok = 16 * (g >> 1) + 2 * (NJ * half + j) + (g & 1);
+                        const int gr = D == 128 ? ((2 * t4 + i) ^ (tok & 7)) : t4;
+                        w[j] = *reinterpret_cast<const uint4 *>(kp + tok * D + gr * 16);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int a = 2 * (4 * i + y);
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            const uint32_t k4 = u4w(w[j], y);
+                            mma16816(sc[j], qf[0][a], qf[1][a], qf[0][a + 1], qf[1][a + 1],
+                                     e4m3x2_to_f16x2(static_cast<uint16_t>(k4)), e4m3x2_to_f16x2(static_cast<uint16_t>(k4 >> 16)));
+                        }
                     }
                 }
-            }
-            // in log2 units, masked; their maximum
-            const bool edge = (pg + 1) * kPage > tile_sees;
-            const float lv = scale_log2(vs), pv = vs * 256.f;
-            float fs[NX], mx[NX];
+                // in log2 units, masked; their maximum
+                const bool edge = (pg + 1) * kPage > tile_sees;
+                const float lv = scale_log2(vs), pv = vs * 256.f;
+                float fs[NX], mx[NX];
 #pragma unroll
-            for (int x = 0; x < NX; ++x) {
-                fs[x] = qs[x] * ks;
-                mx[x] = -INFINITY;
-            }
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int x = 0; x < 2 * NX; ++x) {
-                    sc[j][x] *= fs[x >> 1];
-                    if (edge && pg * kPage + 16 * t4 + 2 * (NJ * half + j) + (x & 1) >= sees[x >> 1]) sc[j][x] = -INFINITY;
-                    mx[x >> 1] = fmaxf(mx[x >> 1], sc[j][x]);
-                }
-            float ref[NX], alpha[NX];
-            bool grew = false;
-#pragma unroll
-            for (int x = 0; x < NX; ++x) {
-                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
-                const float mn = fmaxf(m[x], mx[x] + lv);
-                ref[x] = mn == -INFINITY ? 0.f : mn;
-                alpha[x] = ex2(m[x] - ref[x]);  // m = -inf: 0
-                grew |= mn != m[x];
-                m[x] = mn;
-            }
-            if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                for (int x = 0; x < NX; ++x) l[x] *= alpha[x];
-#pragma unroll
-                for (int i = 0; i < DT; ++i)
-#pragma unroll
-                    for (int x = 0; x < 2 * NX; ++x) o[i][x] *= alpha[x >> 1];
-            }
-            uint32_t pf[2][NJ];  // weights: [row][token pair]
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (x < NX) {
-                        const int y = x < NX ? x : 0;
-                        const float a = ex2(sc[j][2 * y] - ref[y]), b = ex2(sc[j][2 * y + 1] - ref[y]);
-                        l[y] += a + b;
-                        pf[x][j] = cvt_f16x2(a * pv, b * pv);
-                    } else {
-                        pf[x][j] = 0u;
-                    }
+                for (int x = 0; x < NX; ++x) {
+                    fs[x] = qs[x] * ks;
+                    mx[x] = -INFINITY;
                 }
 #pragma unroll
-            for (int i0 = 0; i0 < DT; i0 += 8) {
-                uint2 w[8];
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = *reinterpret_cast<const uint2 *>(vp + (8 * (i0 + i) + g) * kPage + 16 * t4 + 8 * half);
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t v4 = y ? w[i].y : w[i].x;
-                        mma16816(o[i0 + i], pf[0][2 * y], pf[1][2 * y], pf[0][2 * y + 1], pf[1][2 * y + 1],
-                                 e4m3x2_to_f16x2(static_cast<uint16_t>(v4)), e4m3x2_to_f16x2(static_cast<uint16_t>(v4 >> 16)));
+                    for (int x = 0; x < 2 * NX; ++x) {
+                        sc[j][x] *= fs[x >> 1];
+                        if (edge && pg * kPage + 16 * t4 + 2 * (NJ * half + j) + (x & 1) >= sees[x >> 1]) sc[j][x] = -INFINITY;
+                        mx[x >> 1] = fmaxf(mx[x >> 1], sc[j][x]);
                     }
+                float ref[NX], alpha[NX];
+                bool grew = false;
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+                    mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+                    const float mn = fmaxf(m[x], mx[x] + lv);
+                    ref[x] = mn == -INFINITY ? 0.f : mn;
+                    alpha[x] = ex2(m[x] - ref[x]);  // m = -inf: 0
+                    grew |= mn != m[x];
+                    m[x] = mn;
+                }
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) l[x] *= alpha[x];
+#pragma unroll
+                    for (int i = 0; i < DT; ++i)
+#pragma unroll
+                        for (int x = 0; x < 2 * NX; ++x) o[i][x] *= alpha[x >> 1];
+                }
+                uint32_t pf[2][NJ];  // weights: [row][token pair]
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (x < NX) {
+                            const int y = x < NX ? x : 0;
+                            const float a = ex2(sc[j][2 * y] - ref[y]), b = ex2(sc[j][2 * y + 1] - ref[y]);
+                            l[y] += a + b;
+                            pf[x][j] = cvt_f16x2(a * pv, b * pv);
+                        } else {
+                            pf[x][j] = 0u;
+                        }
+                    }
+#pragma unroll
+                for (int i0 = 0; i0 < DT; i0 += 8) {
+                    uint2 w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = *reinterpret_cast<const uint2 *>(vp + (8 * (i0 + i) + g) * kPage + 16 * t4 + 8 * half);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t v4 = y ? w[i].y : w[i].x;
+                            mma16816(o[i0 + i], pf[0][2 * y], pf[1][2 * y], pf[0][2 * y + 1], pf[1][2 * y + 1],
+                                     e4m3x2_to_f16x2(static_cast<uint16_t>(v4)), e4m3x2_to_f16x2(static_cast<uint16_t>(v4 >> 16)));
+                        }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ct->empty[st]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ct->empty[st]);
-        }
-        it0 += s.pe - s.p0;
+            it0 += s.pe - s.p0;
 
-        // ---- the warps' sums to shared memory, added in warp order, CC columns at a time
-        float *mo = mrg, *mm = mrg + kWarps * TR * (CC + 4), *ml = mm + kWarps * TR;
-        float *part = part_slot(p, blockIdx.x, s.p0 == 0);
-#pragma unroll
-        for (int x = 0; x < NX; ++x) {
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-        }
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += CC) {
-            __syncwarp();
-            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last reads are over
+            // ---- the warps' sums to shared memory, added in warp order, CC columns at a time
+            float *mo = mrg, *mm = mrg + kWarps * TR * (CC + 4), *ml = mm + kWarps * TR;
+            float *part = part_slot(p, blockIdx.x, s.p0 == 0);
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
-                const int rr = wid * TR + 8 * x + g;
-                if (t4 == 0) {
-                    mm[rr] = m[x];
-                    ml[rr] = l[x];
-                }
-#pragma unroll
-                for (int i = 0; i < CC / 8; ++i)
-                    *reinterpret_cast<float2 *>(mo + rr * (CC + 4) + 8 * i + 2 * t4) =
-                        make_float2(o[c0 / 8 + i][2 * x], o[c0 / 8 + i][2 * x + 1]);
+                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
             }
-            __syncwarp();
-            asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-            for (int i = tid; i < TR * (CC / 2); i += kConsumers) {
-                const int rr = i / (CC / 2), cc = 2 * (i % (CC / 2)), d = c0 + cc, r = s.tile * TR + rr;
-                float mv = -INFINITY, lv = 0.f, a = 0.f, b = 0.f;
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) mv = fmaxf(mv, mm[k * TR + rr]);
-                const float ref = mv == -INFINITY ? 0.f : mv;
+            for (int c0 = 0; c0 < D; c0 += CC) {
+                __syncwarp();
+                asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");  // the last reads are over
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const int q = k * TR + rr;
-                    const float f = ex2(mm[q] - ref);
-                    const float2 v = *reinterpret_cast<const float2 *>(mo + q * (CC + 4) + cc);
-                    lv += ml[q] * f;
-                    a += v.x * f;
-                    b += v.y * f;
-                }
-                if (!s.whole()) {
-                    *reinterpret_cast<float2 *>(part_at(part, TR, rr, d)) = make_float2(a, b);
-                    if (d == 0) {
-                        part[rr] = mv;
-                        part[TR + rr] = lv;
+                for (int x = 0; x < NX; ++x) {
+                    const int rr = wid * TR + 8 * x + g;
+                    if (t4 == 0) {
+                        mm[rr] = m[x];
+                        ml[rr] = l[x];
                     }
-                } else if (r < rows) {
-                    const float inv = inv_sum(256.f, lv);
-                    *reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, r) + d) = pack_bf16(a * inv, b * inv);
+#pragma unroll
+                    for (int i = 0; i < CC / 8; ++i)
+                        *reinterpret_cast<float2 *>(mo + rr * (CC + 4) + 8 * i + 2 * t4) =
+                            make_float2(o[c0 / 8 + i][2 * x], o[c0 / 8 + i][2 * x + 1]);
+                }
+                __syncwarp();
+                asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+                for (int i = tid; i < TR * (CC / 2); i += kConsumers) {
+                    const int rr = i / (CC / 2), cc = 2 * (i % (CC / 2)), d = c0 + cc, r = s.tile * TR + rr;
+                    float mv = -INFINITY, lv = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) mv = fmaxf(mv, mm[k * TR + rr]);
+                    const float ref = mv == -INFINITY ? 0.f : mv;
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) {
+                        const int q = k * TR + rr;
+                        const float f = ex2(mm[q] - ref);
+                        const float2 v = *reinterpret_cast<const float2 *>(mo + q * (CC + 4) + cc);
+                        lv += ml[q] * f;
+                        a += v.x * f;
+                        b += v.y * f;
+                    }
+                    if (!s.whole()) {
+                        *reinterpret_cast<float2 *>(part_at(part, TR, rr, d)) = make_float2(a, b);
+                        if (d == 0) {
+                            part[rr] = mv;
+                            part[TR + rr] = lv;
+                        }
+                    } else if (r < rows) {
+                        const float inv = inv_sum(256.f, lv);
+                        *reinterpret_cast<uint32_t *>(out_row(p, q0, s.h, G, r) + d) = pack_bf16(a * inv, b * inv);
+                    }
                 }
             }
+            if (!s.whole()) join_tile<D, kConsumers, TR>(p, s, U, blocks, rows, q0, G, 256.f, &ct->last, tid);
         }
-        if (!s.whole()) join_tile<D, kConsumers, TR>(p, s, U, blocks, rows, q0, G, 256.f, &ct->last, tid);
+    }
+
+    // Every copy was waited for by the warp that uses it, unless the block gave up: no block
+    // ends with a copy into its shared memory in flight.  (Asked where all warps have met:
+    // nobody waits for a page, and so gives up, any more.)
+    __syncwarp();
+    __syncthreads();
+    if (*reinterpret_cast<volatile int *>(&ct->abort) && (wid == kWarps || wid == kWarps + 2) && lane == 0) {
+        const int odd = (wid - kWarps) >> 1;
+        const uint64_t t0 = gtimer();
+        ring_drain_halves(
+            odd, ct->issued[2 * odd], ct->issued[2 * odd + 1], NS, [&](int st) { mbar_arrive(&ct->full[st]); },
+            [&](int st, uint32_t parity) {
+                while (!mbar_test(&ct->full[st], parity) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
+                }
+            });
     }
 }
 

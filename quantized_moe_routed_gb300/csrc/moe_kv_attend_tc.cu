@@ -38,6 +38,7 @@
 // scores, 580 us for 2048 x 16384 tokens and 32 heads.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
+#include "moe_ring.h"
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -82,6 +83,7 @@ struct Control {
     float ref[2][kRows];                   // the reference after a warpgroup's last step
     float l[2][kRows], lref[2][kRows];     // the warpgroups' sums at a tile's end and what they refer to
     uint32_t tmem;
+    int issued[2];                         // steps whose k and whose v were issued
     int abort, last;
 };
 
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const bool values = wid != kProducer;
             const int stages = values ? kVStages : kKStages;
             uint64_t *full = values ? ct->v_full : ct->k_full, *empty = values ? ct->v_empty : ct->k_empty;
-            int it = 0, st = 0;
+            int it = 0, st = 0, issued = 0;
             uint32_t phase = 1;
             const uint64_t pol = policy_evict_last();  // other tiles read the page too
             for (long long u = u0; u < u1;) {
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                                     }
                                     mbar_arrive(&ct->sc_full[sc]);
                                 }
+                                issued = it + 1;
                             }
                         }
                         if (++st == stages) st = 0, phase ^= 1;
@@ -379,14 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 }
                 u += s.units;
             }
-            if (lane == 0 && aborted()) {
-                // no block ends with a copy into its shared memory in flight
-                const uint64_t t0 = gtimer();
-                for (int j = max(it - stages, 0); j < it; ++j)
-                    while (!mbar_test(&full[j % stages], (j / stages) & 1) &&
-                           static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
-                    }
-            }
+            if (lane == 0) ct->issued[values] = issued;
         } else if (wid == kIssuer || wid == kIssuer + 1) {
             // ---- MMA issue, a warp for S and one for O, an elected lane of each.  A
             // block that gave up goes on without waiting, on whatever is there.
@@ -442,13 +438,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     }
                 }
                 __syncwarp();
-            }
-            if (__any_sync(0xffffffffu, aborted()) && elect_one()) {
-                // no block ends with products in flight
-                tc_commit(&ct->drained[scores]);
-                const uint64_t t0 = gtimer();
-                while (!mbar_test(&ct->drained[scores], 0) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
-                }
             }
         }
     } else {
@@ -652,6 +641,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // No block ends with a copy into its shared memory or a product in flight: each was waited
+    // for, unless the block gave up.  (Asked where all warps have met: nobody waits, and
+    // so gives up, any more.)
+    if (aborted()) {
+        const uint64_t t0 = gtimer();
+        auto landed = [&](uint64_t *bar, uint32_t parity) {
+            while (!mbar_test(bar, parity) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
+            }
+        };
+        if (wid == kProducer && lane == 0)
+            ring_drain(ct->issued[0], kKStages, [&](int st, uint32_t parity) { landed(&ct->k_full[st], parity); });
+        if (wid == kProducer + 1 && lane == 0)
+            ring_drain(ct->issued[1], kVStages, [&](int st, uint32_t parity) { landed(&ct->v_full[st], parity); });
+        if ((wid == kIssuer || wid == kIssuer + 1) && elect_one()) {  // (the lane that issued them)
+            tc_commit(&ct->drained[wid - kIssuer]);
+            landed(&ct->drained[wid - kIssuer], 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
     if (wid == kIssuer) tc_dealloc(tmem, kTmemCols);
 }
 

@@ -29,6 +29,7 @@
 // A wait that runs out (bounded as everywhere) leaves NaN in the block's rows.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
+#include "moe_ring.h"
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -70,6 +71,7 @@ struct Control {
     uint64_t d_ready, drained[2];
     uint32_t amax[32];          // largest magnitude of each token, as bits
     uint32_t tmem;
+    int issued;                 // stages of weights that were issued
     int abort;
 };
 
@@ -165,18 +167,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
                 for (int m = 0; m < tiles; ++m, ++it) {
                     const int st = it % NS;
                     if (it >= NS) wait(&ct->empty[st], (it / NS - 1) & 1);
-                    if (aborted()) goto out;
+                    if (aborted()) goto out;  // (what is issued stays a run from the first on)
                     mbar_expect_tx(&ct->full[st], tp.rows * (kPiece / 2));
                     tma2d(codes + st * kCodes, &tp.tm_q, k * (kPiece / 2), row0 + m * tp.rows, &ct->full[st], pol);
                 }
         out:
-            if (aborted()) {
-                // no block ends with a copy into its shared memory in flight
-                const uint64_t t0 = gtimer();
-                for (int j = max(it - NS, 0); j < it; ++j)
-                    while (!mbar_test(&ct->full[j % NS], (j / NS) & 1) && static_cast<long long>(gtimer() - t0) < tp.timeout_ns) {
-                    }
-            }
+            ct->issued = it;
         }
     } else {
         // ---- each token's largest element: a warp takes 256 elements of a token at a time
@@ -252,16 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
             }
             if (elect_one()) tc_commit(&ct->x_empty[k & 1]);
         }
-        if (elect_one()) {
-            tc_commit(&ct->d_ready);
-            if (aborted()) {
-                // no block ends with products in flight
-                tc_commit(&ct->drained[w]);
-                const uint64_t t0 = gtimer();
-                while (!mbar_test(&ct->drained[w], 0) && static_cast<long long>(gtimer() - t0) < tp.timeout_ns) {
-                }
-            }
-        }
+        if (elect_one()) tc_commit(&ct->d_ready);
     } else if (wid >= kStager && wid < kConverter) {
         // ---- x: items of 8 elements, item i is token i / 32, elements 8 (i % 32) .. of the piece
         constexpr int kItems = TN * kPiece / 8 / 128;
@@ -434,6 +421,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
     __syncwarp();
     __syncthreads();
     tc_fence_after();
+    // No block ends with a copy into its shared memory or a product in flight: each was waited
+    // for, unless the block gave up.  (Asked where all warps have met: nobody waits, and
+    // so gives up, any more.)
+    if (aborted()) {
+        const uint64_t t0 = gtimer();
+        auto landed = [&](uint64_t *bar, uint32_t parity) {
+            while (!mbar_test(bar, parity) && static_cast<long long>(gtimer() - t0) < tp.timeout_ns) {
+            }
+        };
+        if (wid == kProducer && lane == 0)
+            ring_drain(ct->issued, NS, [&](int st, uint32_t parity) { landed(&ct->full[st], parity); });
+        if ((wid == kIssuer || wid == kIssuer + 1) && elect_one()) {  // (the lane that issued them)
+            tc_commit(&ct->drained[wid - kIssuer]);
+            landed(&ct->drained[wid - kIssuer], 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
     if (wid == kIssuer) tc_dealloc(tmem, kTmemCols);
 }
 
