@@ -275,21 +275,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    grid_wait();
-    grid_release();
-    plan_units<kTileCost>(p, sq, G, TR);
-    const long long U = sq.cum[c.B];
-    const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
-    if (static_cast<int>(blockIdx.x) >= blocks) return;
-    const long long u0 = block_start(U, blocks, blockIdx.x), u1 = block_start(U, blocks, blockIdx.x + 1);
     // first warps of each kind (where several are ready the older issues, and
     // everything waits for the producer and the issuers)
     constexpr int kProducer = 0, kIssuer = 2, kConverter = 4, kSoftmax = 8;
+    // tensor memory before the next kernel may start: its blocks can take theirs ahead of
+    // their wait for this one, which must not have to wait for them in turn
     if (wid == kIssuer) tc_alloc(&ct->tmem, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ct->tmem;
+    grid_wait();
+    grid_release();
+    plan_units<kTileCost>(p, sq, G, TR);
+    const long long U = sq.cum[c.B];
+    const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        if (wid == kIssuer) tc_dealloc(tmem, kTmemCols);
+        return;
+    }
+    const long long u0 = block_start(U, blocks, blockIdx.x), u1 = block_start(U, blocks, blockIdx.x + 1);
 
     if (wid < kSoftmax) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));

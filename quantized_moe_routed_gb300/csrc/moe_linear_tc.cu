@@ -150,12 +150,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_linear_tc_kernel(const __grid
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid < TN) ct->amax[tid] = 0;
+    // tensor memory before the next kernel may start: its blocks can take theirs ahead of
+    // their wait for this one (as these do), which must not have to wait for them in turn
     if (wid == kIssuer) tc_alloc(&ct->tmem, kTmemCols);
-    grid_wait();
-    grid_release();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();
+    grid_release();
     const uint32_t tmem = ct->tmem, ta = tmem + kTmemCols - 2 * NB * 64;
 
     if (wid == kProducer) {
