@@ -5,8 +5,9 @@ included) and the attention over it.
 
 Argument marshalling only, as in `binding`: every step of the computation runs
 in the library's sm_103a kernels, on `stream` or the current stream; outputs
-that the caller does not pass are allocated on that stream.  A call that fails
-raises MoeError; there is no fallback.
+that the caller does not pass are allocated on that stream.  Tensors and stream
+belong to the current device.  A call that fails raises MoeError; there is no
+fallback.
 """
 from __future__ import annotations
 
@@ -104,8 +105,15 @@ def _empty(shape, dtype, device, stream):
 
 
 def _handle(stream, device):
-    """cudaStream_t of `stream`, or of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    """cudaStream_t of `stream`, or of the device's current stream.  The kernels
+    launch on the current device, which has to be the tensors'."""
+    if device.index != torch.cuda.current_device():
+        raise _bad(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise _bad(f"a stream of {stream.device} for tensors on {device}")
+    return stream.cuda_stream
 
 
 def _ptr(t):
@@ -133,6 +141,7 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, residual_out=None,
     T, H = x.shape
     stride = _rows(x, (torch.float32, torch.bfloat16), (H,), "x")
     dev = x.device
+    handle = _handle(stream, dev)
     _need_out(weight, torch.bfloat16, (H,), dev, "weight")
     if residual is None:
         if residual_out is not None:
@@ -161,8 +170,7 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, residual_out=None,
         _need_out(out_q, torch.float8_e4m3fn, (T, H), dev, "out_q")
         _need_out(out_scale, torch.float32, (T, H // 128), dev, "out_scale")
     st = _library().moe_norm(x.data_ptr(), x.dtype == torch.float32, stride, _ptr(residual), _ptr(residual_out),
-                             weight.data_ptr(), eps, _ptr(out), _ptr(out_q), _ptr(out_scale), T, H,
-                             _handle(stream, dev))
+                             weight.data_ptr(), eps, _ptr(out), _ptr(out_q), _ptr(out_scale), T, H, handle)
     if st != MOE_OK:
         _check(st)
     return out if outputs == "bf16" else ((out_q, out_scale) if outputs == "e4m3" else (out, out_q, out_scale))
@@ -193,6 +201,7 @@ class Nvfp4Linear:
         stride = _rows(x, _BF16, (self.K,), "x")
         if x.device != dev:
             _same_device(dev, x=x)
+        handle = _handle(stream, dev)
         T = x.shape[0]
         if out is not None:
             dtype = out.dtype
@@ -203,7 +212,7 @@ class Nvfp4Linear:
         else:
             _need_out(out, dtype, (T, self.N), dev, "out")
         st = _library().moe_linear(*self._weights, x.data_ptr(), stride, out.data_ptr(), dtype == torch.bfloat16, T,
-                                   _handle(stream, dev))
+                                   handle)
         if st != MOE_OK:
             _check(st)
         return out
@@ -276,8 +285,9 @@ class KVCache:
 
     def new_workspace(self, stream=None) -> torch.Tensor:
         """Zeroed workspace for append and attend: one per concurrent stream."""
+        handle = _handle(stream, self.device)
         ws = _empty((self._ws_bytes,), torch.uint8, self.device, stream)
-        _check(_library().moe_kv_workspace_init(self.handle, ws.data_ptr(), self._ws_bytes, _handle(stream, self.device)))
+        _check(_library().moe_kv_workspace_init(self.handle, ws.data_ptr(), self._ws_bytes, handle))
         return ws
 
     def _step(self, q_off, kv_len, pages, ws, N, max_q):
@@ -312,6 +322,7 @@ class KVCache:
         qs = 0
         if k.device != dev or v.device != dev:
             _same_device(dev, k=k, v=v)
+        handle = _handle(stream, dev)
         if q is not None:
             qs = _rows(q, _BF16, self._q_row, "q", N)
             if q.device != dev:
@@ -323,8 +334,7 @@ class KVCache:
         elif q_out is not None:
             raise _bad("q_out without q")
         st = _library().moe_kv_append(self.handle, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_out),
-                                      self._step(q_off, kv_len, pages, ws, N, max_q), ws.data_ptr(),
-                                      _handle(stream, dev))
+                                      self._step(q_off, kv_len, pages, ws, N, max_q), ws.data_ptr(), handle)
         if st != MOE_OK:
             _check(st)
         return q_out
@@ -337,13 +347,14 @@ class KVCache:
         qs = _rows(q, _BF16, self._q_row, "q")
         if q.device != dev:
             _same_device(dev, q=q)
+        handle = _handle(stream, dev)
         if out is None:
             out = _empty(q.shape, torch.bfloat16, dev, stream)
         else:
             _need_out(out, torch.bfloat16, q.shape, dev, "out")
         st = _library().moe_kv_attend(self.handle, q.data_ptr(), qs, self._scale if scale is None else scale,
                                       out.data_ptr(), self._step(q_off, kv_len, pages, ws, q.shape[0], max_q),
-                                      ws.data_ptr(), _handle(stream, dev))
+                                      ws.data_ptr(), handle)
         if st != MOE_OK:
             _check(st)
         return out
