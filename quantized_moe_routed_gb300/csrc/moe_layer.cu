@@ -72,6 +72,17 @@ moe_status_t launched(cudaError_t e, const char *what)
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// What is queued goes to the current device: it has to be the cache's.
+moe_status_t check_device(moe_kv_t kv)
+{
+    int cur = -1;
+    const cudaError_t e = cudaGetDevice(&cur);
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    if (cur != kv->device)
+        return fail(MOE_ERR_INVALID_ARG, "current device %d is not the cache's device %d", cur, kv->device);
+    return MOE_OK;
+}
+
 moe_status_t check_kv(moe_kv_t kv, const moe_kv_batch *b, const void *ws)
 {
     if (!kv || !b) return fail(MOE_ERR_INVALID_ARG, "null cache or batch");
@@ -87,12 +98,7 @@ moe_status_t check_kv(moe_kv_t kv, const moe_kv_batch *b, const void *ws)
         return fail(MOE_ERR_INVALID_ARG, "null q_off/kv_len/pages/workspace pointer");
     if (!aligned(b->q_off_dev, 4) || !aligned(b->kv_len_dev, 4) || !aligned(b->pages_dev, 4) || !aligned(ws, 256))
         return fail(MOE_ERR_MISALIGNED, "int32 arrays need 4-byte, the workspace 256-byte alignment");
-    int cur = -1;
-    const cudaError_t e = cudaGetDevice(&cur);
-    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-    if (cur != kv->device)
-        return fail(MOE_ERR_INVALID_ARG, "current device %d is not the cache's device %d", cur, kv->device);
-    return MOE_OK;
+    return check_device(kv);
 }
 
 moe_status_t check_rows(const void *ptr, int64_t stride, int64_t row, const char *name)
@@ -259,8 +265,10 @@ moe_status_t moe_kv_workspace_init(moe_kv_t kv, void *ws_dev, size_t bytes, void
     if (!aligned(ws_dev, 256)) return fail(MOE_ERR_MISALIGNED, "workspace must be 256-byte aligned");
     if (bytes < kv->ws_bytes)
         return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed", bytes, kv->ws_bytes);
+    moe_status_t st = check_device(kv);
+    if (st != MOE_OK) return st;
     moe::WsTicket tk;
-    const moe_status_t st = moe::ws_claim(ws_dev, static_cast<cudaStream_t>(stream), tk);
+    st = moe::ws_claim(ws_dev, static_cast<cudaStream_t>(stream), tk);
     if (st != MOE_OK) return st;
     // the partial results behind the counters are written before they are read
     const cudaError_t e = cudaMemsetAsync(ws_dev, 0, kv->off_part, static_cast<cudaStream_t>(stream));
@@ -324,6 +332,8 @@ moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, flo
 moe_status_t moe_kv_check(moe_kv_t kv, void *ws_dev, void *stream)
 {
     if (!kv || !ws_dev) return fail(MOE_ERR_INVALID_ARG, "null cache or workspace");
+    const moe_status_t st = check_device(kv);
+    if (st != MOE_OK) return st;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     uint8_t *word_dev = static_cast<uint8_t *>(ws_dev) + 8;
     uint32_t word = 0;
