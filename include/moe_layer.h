@@ -141,8 +141,9 @@ moe_status_t moe_kv_workspace_init(moe_kv_t kv, void *ws_dev, size_t bytes, void
  * in bf16, head_dim and heads contiguous, tokens q_stride, k_stride and
  * v_stride elements apart (slices of one projection's output): 16-byte aligned
  * pointers, strides multiples of 8 and at least a token's elements.
- *   q_out  bf16 [N, q_heads, head_dim] contiguous: the rotated queries (q and
- *          q_out both NULL: keys and values only)
+ *   q_out  bf16 [N, q_heads, head_dim] contiguous: the rotated queries, may be q
+ *          itself where that is contiguous too (q and q_out both NULL: keys and
+ *          values only)
  * Rotations are in fp32 (each product and sum rounded); keys are quantised from
  * there.  In each page and head that gets new tokens the scale is the smallest
  * power of two (2^-64 .. 2^60) with |values| <= 448 scale over the new ones,

@@ -249,6 +249,9 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
                 for (int g = 0; g < G; ++g) {
                     float v[16];
                     if (turns) load_unit<ROT>(c, v, src + g * D, un, cs, pos0 + tok);
+                    // where partners are other elements of the token's UT lanes, all are read before
+                    // any is written: the queries may be rotated in place
+                    if (ROT == kOddHalves) __syncwarp(((1u << UT) - 1u) << (tid & 31 & ~(UT - 1)));
                     if (!turns || id < 0 || id >= c.n_pages) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = 0.f;
