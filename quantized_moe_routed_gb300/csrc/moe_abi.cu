@@ -1153,6 +1153,8 @@ const char *moe_status_string(moe_status_t s)
         case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT";
         case MOE_ERR_BAD_EXPERT_ID: return "MOE_ERR_BAD_EXPERT_ID";
         case MOE_ERR_RANGE: return "MOE_ERR_RANGE";
+        case MOE_ERR_SCALE: return "MOE_ERR_SCALE";
+        case MOE_ERR_WORKSPACE_BUSY: return "MOE_ERR_WORKSPACE_BUSY";
         case MOE_ERR_BAD_INDEX: return "MOE_ERR_BAD_INDEX";
     }
     return "MOE_ERR_UNKNOWN";
