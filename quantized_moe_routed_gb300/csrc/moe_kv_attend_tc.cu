@@ -21,6 +21,12 @@
 // step exceeds it by more than 8 (fp16 holds 64 * 2^8), so the accumulators in
 // tensor memory are rescaled rarely.
 //
+// The tensor cores' additions cut what does not fit instead of rounding it: O loses 6e-9 of
+// itself a token (weights and values of one sign; 0.6% over a million tokens in one run,
+// more than a bf16 output's rounding).  So a run ends after 128 steps: O then goes on in additions
+// that round, in the block's place for partial results (no column of tensor memory is
+// left), and starts over; 1e-4 is lost.
+//
 // A group of eight MMAs takes 800 cycles from issue to its barrier, 512 of them at
 // work, and a softmax step about 1700: so steps overlap.  Two warpgroups take the
 // steps in turn (a thread a row), each with its own S and P in tensor memory; the
@@ -69,6 +75,8 @@ constexpr int kTmemCols = 512, kTmemP = 256, kTmemO = 384;
 // in pages: about 14000 cycles against 900 a page.
 constexpr int kTileCost = 16;
 constexpr int kKStages = 3, kVStages = 4, kFStages = 2;  // steps of k, of v, of v in fp16
+constexpr int kRun = 128;        // steps whose weighted sums are added up on the tensor cores: even, so that
+                                 // of a segment the same warpgroup ends every run
 constexpr int kScales = 8;       // steps whose scales are kept: more than a softmax lags behind the producer
 
 struct Control {
@@ -82,6 +90,7 @@ struct Control {
     float qs[kRows];                       // each row's factor from digits to scores (log2 units)
     float ref[2][kRows];                   // the reference after a warpgroup's last step
     float l[2][kRows], lref[2][kRows];     // the warpgroups' sums at a tile's end and what they refer to
+    float kref[kRows];                     // what the weighted sums of ended runs refer to
     uint32_t tmem;
     int issued[2];                         // steps whose k and whose v were issued
     int abort, last;
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                         wait_or_abort(&ct->p_ready[b], (n / 2) & 1, p, &ct->abort);
                         __syncwarp();
                         tc_fence_after();
-                        const uint32_t add = i > 0;
+                        const uint32_t add = i % kRun != 0;
                         if (elect_one()) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)  // 16 tokens each: four of each page
@@ -483,6 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const int tile_sees = row_sees(len, n, G, row0);  // the least of the tile's rows
 
             float l = 0.f, lref = -INFINITY;  // this warpgroup's sum and what it refers to
+            // (a run's end is a step of the segment's first warpgroup)
+            if (w == (n0 & 1)) ct->kref[row] = -INFINITY;
             for (int i = (n0 & 1) == w ? 0 : 1; i < steps; i += 2) {
                 const uint32_t k = n0 + i, ph = (k >> 1) & 1, sc = k % kScales;  // step, its barriers' phase
                 wait_or_abort(&ct->sc_full[sc], (k / kScales) & 1, p, &ct->abort);
@@ -542,22 +553,38 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     __syncwarp();
                     tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, move) && i > 0) {
-                    // the accumulators follow, between the last step's product and this one's
+                const bool ends = i > 0 && i % kRun == 0;  // the run before this step
+                const bool moves = i > 0 && __any_sync(0xffffffffu, move);
+                if (ends || moves) {
+                    // the accumulators follow, between the last step's product and this one's:
+                    // they go on under the new reference, or where the ended runs' sums are
                     wait_or_abort(&ct->o_ready[w ^ 1], ((k - 1) >> 1) & 1, p, &ct->abort);
                     __syncwarp();
                     tc_fence_after();
-                    const float f = move ? ex2(old - ref) : 1.f;
+                    const float kref = ct->kref[row];
+                    const float f = ends ? (kref == -INFINITY ? 0.f : ex2(kref - old)) : (move ? ex2(old - ref) : 1.f);
 #pragma unroll 1
                     for (int h = 0; h < D / 16; ++h) {
                         float v[16];
-                        uint32_t x[16];
                         tc_ld16(to + 16 * h, v);
                         tc_wait_ld();
+                        if (ends) {
+                            float *part = part_slot(p, blockIdx.x, s.p0 == 0);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(v[j] * f);
-                        tc_st16(to + 16 * h, x);
+                            for (int j = 0; j < 4; ++j) {
+                                float4 *at = reinterpret_cast<float4 *>(part_at(part, TR, row, 16 * h + 4 * j));
+                                const float4 was = i > kRun ? __ldcg(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                __stcg(at, make_float4(fmaf(was.x, f, v[4 * j]), fmaf(was.y, f, v[4 * j + 1]),
+                                                       fmaf(was.z, f, v[4 * j + 2]), fmaf(was.w, f, v[4 * j + 3])));
+                            }
+                        } else {
+                            uint32_t x[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(v[j] * f);
+                            tc_st16(to + 16 * h, x);
+                        }
                     }
+                    if (ends) ct->kref[row] = old;
                 }
                 const float base = ref == -INFINITY ? 0.f : ref;
                 if (lref != ref) l *= ex2(lref - base);  // (lref = -inf: 0, as l is)
@@ -598,12 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             __syncwarp();
             asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
             n0 += steps;
-            float ref = -INFINITY, lsum = 0.f;
+            float ref = -INFINITY, lsum = 0.f, kf = 0.f;
             if (steps > 0) {
                 const uint32_t last = n0 - 1;
                 ref = ct->ref[last & 1][row];
                 const float base = ref == -INFINITY ? 0.f : ref;
                 lsum = ct->l[0][row] * ex2(ct->lref[0][row] - base) + ct->l[1][row] * ex2(ct->lref[1][row] - base);
+                if (ct->kref[row] != -INFINITY) kf = ex2(ct->kref[row] - base);
                 wait_or_abort(&ct->o_ready[last & 1], (last >> 1) & 1, p, &ct->abort);  // (products end in order)
                 __syncwarp();
                 tc_fence_after();
@@ -623,6 +651,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 for (int j = 0; j < 16; ++j) v[j] = 0.f;
                 if (steps > 0) tc_ld16(to + col, v);
                 tc_wait_ld();
+                if (steps > kRun) {  // the ended runs
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 was = __ldcg(reinterpret_cast<const float4 *>(part_at(part, TR, row, col + 4 * j)));
+                        v[4 * j] = fmaf(was.x, kf, v[4 * j]);
+                        v[4 * j + 1] = fmaf(was.y, kf, v[4 * j + 1]);
+                        v[4 * j + 2] = fmaf(was.z, kf, v[4 * j + 2]);
+                        v[4 * j + 3] = fmaf(was.w, kf, v[4 * j + 3]);
+                    }
+                }
                 if (!s.whole()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
