@@ -170,10 +170,11 @@ moe_status_t moe_kv_append(moe_kv_t kv, const void *q_dev, int64_t q_stride, con
  * codes' exact values.  With up to 16 rows (a sequence's new tokens x query heads
  * of a kv head) q enters as fp16 (exact for elements down to 2^-28 of the row's
  * largest), with more as the sum of two E4M3 digits (exact down to 2^-10 of it);
- * softmax weights are rounded to fp16 (2^-12 of each, or 2^-31 of the row's
- * largest if more); sums, maxima and the softmax in fp32, where the additions of the
- * second product cut instead of rounding: values of one sign lose up to 2^-12 of their sum with more
- * than 16 rows, 2^-30 a token (of those that one block adds up) with up to 16.  A page id out of range counts
+ * softmax weights are rounded to fp16 (2^-11 of each, or 2^-30 of the row's largest weight x
+ * scale of v if more); sums, maxima and the softmax in fp32, where the additions of
+ * the second product cut instead of rounding: values of one sign lose up to 2^-12 of
+ * their sum with more than 16 rows, 2^-30 a token (of those that one block adds up)
+ * with up to 16.  A page id out of range counts
  * as tokens that nothing sees and is flagged for moe_kv_check. */
 moe_status_t moe_kv_attend(moe_kv_t kv, const void *q_dev, int64_t q_stride, float scale, void *o_dev,
                            const moe_kv_batch *batch, void *ws_dev, void *stream);
