@@ -67,6 +67,8 @@ moe_status_t moe_norm(const void *x_dev, int x_f32, int64_t x_stride, const void
  *   batches: up to 24 tokens read the weights once; more run in groups of 24 (of
  *   32 where the weights have many rows, K is a multiple of 256 and s_dev 16-byte
  *   aligned), each reading them again (from L2 as far as they fit).
+ *   Which kernel runs, and so the order of the sums, depends on T too: the same token
+ *   can have other last bits in a batch of another size.
  *   A device-side wait that ran out (bounded as in moe_nvfp4.h) leaves NaN in the
  *   outputs of its block's rows: this call has no workspace to flag it in.
  * q_dev and x_dev 16-byte aligned, s_dev 2-byte, ts_dev 4-byte, y_dev to its
@@ -169,7 +171,8 @@ moe_status_t moe_kv_append(moe_kv_t kv, const void *q_dev, int64_t q_stride, con
  * Rows of o outside every sequence are not written.  Products use the 8-bit
  * codes' exact values.  With up to 16 rows (a sequence's new tokens x query heads
  * of a kv head) q enters as fp16 (exact for elements down to 2^-28 of the row's
- * largest), with more as the sum of two E4M3 digits (exact down to 2^-10 of it);
+ * largest), with more as the sum of two E4M3 digits (exact for elements down to 2^-9
+ * of it, smaller ones off by at most 2^-17 of it);
  * softmax weights are rounded to fp16 (2^-11 of each, or 2^-30 of the row's largest weight x
  * scale of v if more); sums, maxima and the softmax in fp32, where the additions of
  * the second product cut instead of rounding: values of one sign lose up to 2^-12 of

@@ -10,7 +10,7 @@
 //  * S = Q K^T, kind::f8f6f4 on the cache's E4M3 codes as TMA brings them: q enters
 //    as two E4M3 digits, hi + lo, after a power-of-two prescale of the row (largest
 //    magnitude into [128, 256)): 8 significant bits are two digits of 4, so the
-//    sum is exact down to 2^-10 of the row's largest.  Two digits at twice the
+//    sum is exact down to 2^-9 of the row's largest, smaller elements off by 2^-17 of it.  Two digits at twice the
 //    16-bit rate cost what 16-bit operands would.
 //  * O += P V, kind::f16: the weights 64 w vs (vs: the page's v scale over the largest
 //    that the reference allows for) are rounded to fp16 and written to tensor
