@@ -236,7 +236,8 @@ class KVCache:
     """A paged key/value cache in 8 bits (moe_kv_create): k uint8 [n_pages,
     kv_heads, PAGE, head_dim], v uint8 [n_pages, kv_heads, head_dim, PAGE] (E4M3
     codes, v transposed), k_scale and v_scale float32 [n_pages, kv_heads].
-    Allocated zeroed, or taken from `buffers` (dict of k, v, k_scale, v_scale).
+    Allocated zeroed, or taken from `buffers` (dict of k, v, k_scale, v_scale; v
+    must hold no NaN code, 0x7F or 0xFF, in unused slots either: zero it once).
     rope: float32 [positions, rot_dim] (rope_table) or None for no rotation.
 
     A step's sequences are q_off int32 [B + 1] (offsets of each one's new tokens),
@@ -314,7 +315,9 @@ class KVCache:
     def append(self, k, v, q_off, kv_len, pages, ws, max_q: int, q=None, q_out=None, stream=None):
         """Rotate and append the new tokens' k and v (bfloat16 [N, kv_heads,
         head_dim], tokens may be strided), and rotate q (bfloat16 [N, q_heads,
-        head_dim]) into q_out, which is returned (None without q)."""
+        head_dim]) into q_out, which is returned (None without q) and may be q.
+        Rows outside every sequence (before q_off[0], from q_off[B] on) are not
+        read and not written: a q_out allocated here holds anything there."""
         dev = self.device
         ks = _rows(k, _BF16, self._kv_row, "k")
         N = k.shape[0]
@@ -342,7 +345,10 @@ class KVCache:
     def attend(self, q, q_off, kv_len, pages, ws, max_q: int, scale: float = None, out=None, stream=None):
         """Causal attention of q (bfloat16 [N, q_heads, head_dim], tokens may be
         strided) over the cache: bfloat16 [N, q_heads, head_dim].  scale: 1 /
-        sqrt(head_dim) unless given."""
+        sqrt(head_dim) unless given.  A token that sees nothing gets 0; rows
+        outside every sequence (before q_off[0], from q_off[B] on) are not written:
+        an out allocated here holds anything there, so give a zeroed one where
+        what follows reads padded rows."""
         dev = self.device
         qs = _rows(q, _BF16, self._q_row, "q")
         if q.device != dev:

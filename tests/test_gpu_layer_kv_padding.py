@@ -57,3 +57,29 @@ def test_padding_between_live_sequences(n, D):
     _check_attend(step, bufs, q, out, D ** -0.5)
     empty = torch.tensor([b not in live for b in range(200)]).repeat_interleave(n)
     assert bool((out[empty.to(DEV)] == 0).all())
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_rows_outside_every_sequence_are_left_alone(n):
+    """A step's arrays may be longer than its sequences (padding of a captured batch),
+    in front and behind: those rows are not read, and not written."""
+    step = Step([n, n], [n + 70, n], seed=n)
+    bufs = _pool(step, 2, 128, seed=n)
+    q_off, kv_len, pages = step.dev()
+    N = step.N + 5
+    g = torch.Generator().manual_seed(n)
+    qkv = torch.randn((N, 12, 128), generator=g).bfloat16()
+    qkv[:2], qkv[-3:] = float("nan"), float("nan")
+    q, k, v = qkv.to(DEV).split((8, 2, 2), dim=1)
+    cache, alone = _cache(bufs, 8, 2, 128), _cache(bufs, 8, 2, 128)
+    ws = cache.new_workspace()
+    q_out, out = (torch.full((N, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    cache.append(k, v, q_off + 2, kv_len, pages, ws, n, q=q, q_out=q_out)
+    cache.attend(q_out, q_off + 2, kv_len, pages, ws, n, out=out)
+    assert cache.check(ws) == 0
+    want_q = alone.append(k[2:-3], v[2:-3], q_off, kv_len, pages, ws, n, q=q[2:-3])
+    want = alone.attend(want_q, q_off, kv_len, pages, ws, n)
+    for got, inner in ((q_out, want_q), (out, want)):
+        assert torch.equal(got[2:-3], inner)
+        assert bool((got[:2] == 7).all()) and bool((got[-3:] == 7).all())
+    assert torch.equal(cache.k, alone.k) and torch.equal(cache.v, alone.v)
