@@ -10,8 +10,8 @@
 //  * S = Q K^T, kind::f8f6f4 on the cache's E4M3 codes as TMA brings them: q enters
 //    as two E4M3 digits, hi + lo, after a power-of-two prescale of the row (largest
 //    magnitude into [128, 256)): 8 significant bits are two digits of 4, so the
-//    sum is exact down to 2^-9 of the row's largest, smaller elements off by 2^-17 of it.  Two digits at twice the
-//    16-bit rate cost what 16-bit operands would.
+//    sum is exact down to 2^-9 of the row's largest, smaller elements off by 2^-17 of
+//    it.  Two digits at twice the 16-bit rate cost what 16-bit operands would.
 //  * O += P V, kind::f16: the weights 64 w vs (vs: the page's v scale over the largest
 //    that the reference allows for) are rounded to fp16 and written to tensor
 //    memory.  v's codes become fp16 (exact) in shared memory; two digits for the
@@ -92,7 +92,6 @@ struct Control {
     float l[2][kRows], lref[2][kRows];     // the warpgroups' sums at a tile's end and what they refer to
     float kref[kRows];                     // what the weighted sums of ended runs refer to
     uint32_t tmem;
-    int issued[2];                         // steps whose k and whose v were issued
     int abort, last;
 };
 
@@ -305,6 +304,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     }
     const long long u0 = block_start(U, blocks, blockIdx.x), u1 = block_start(U, blocks, blockIdx.x + 1);
 
+    // No block ends with a copy into its shared memory or a product in flight: each was waited
+    // for, unless the block gave up.  Whoever has some in flight asks where all warps have met:
+    // nobody waits, and so gives up, any more.  (Each kind of warp comes here from its own end:
+    // the same behind their common one slowed the loops, 451 against 437 us for a prefill chunk.)
+    auto meet = [&] {
+        __syncwarp();
+        asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+        return aborted();
+    };
+    auto landed = [&](uint64_t *bar, uint32_t parity, uint64_t t0) {
+        while (!mbar_test(bar, parity) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
+        }
+    };
+
     if (wid < kSoftmax) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (wid >= kConverter) {
@@ -342,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 it = end;
                 u += s.units;
             }
+            meet();
         } else if (wid < kIssuer) {
             // ---- producers, one of k and one of v: two pages a step; an odd last page
             // comes twice (the second copy is behind every row's mask)
@@ -396,7 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 }
                 u += s.units;
             }
-            if (lane == 0) ct->issued[values] = issued;
+            if (meet() && lane == 0) {
+                const uint64_t t0 = gtimer();
+                ring_drain(issued, stages, [&](int st, uint32_t parity) { landed(&full[st], parity, t0); });
+            }
         } else if (wid == kIssuer || wid == kIssuer + 1) {
             // ---- MMA issue, a warp for S and one for O, an elected lane of each.  A
             // block that gave up goes on without waiting, on whatever is there.
@@ -452,6 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                     }
                 }
                 __syncwarp();
+            }
+            if (meet() && elect_one()) {  // (the lane that issued them)
+                tc_commit(&ct->drained[scores]);
+                landed(&ct->drained[scores], 0, gtimer());
             }
         }
     } else {
@@ -679,31 +700,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             tc_fence_before();
             if (!s.whole()) join_tile<D, kConsumers, TR>(p, s, U, blocks, rows, q0, G, kGain, &ct->last, ctid);
         }
+        tc_fence_before();
+        meet();
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // No block ends with a copy into its shared memory or a product in flight: each was waited
-    // for, unless the block gave up.  (Asked where all warps have met: nobody waits, and
-    // so gives up, any more.)
-    if (aborted()) {
-        const uint64_t t0 = gtimer();
-        auto landed = [&](uint64_t *bar, uint32_t parity) {
-            while (!mbar_test(bar, parity) && static_cast<long long>(gtimer() - t0) < p.timeout_ns) {
-            }
-        };
-        if (wid == kProducer && lane == 0)
-            ring_drain(ct->issued[0], kKStages, [&](int st, uint32_t parity) { landed(&ct->k_full[st], parity); });
-        if (wid == kProducer + 1 && lane == 0)
-            ring_drain(ct->issued[1], kVStages, [&](int st, uint32_t parity) { landed(&ct->v_full[st], parity); });
-        if ((wid == kIssuer || wid == kIssuer + 1) && elect_one()) {  // (the lane that issued them)
-            tc_commit(&ct->drained[wid - kIssuer]);
-            landed(&ct->drained[wid - kIssuer], 0);
-        }
-        __syncwarp();
-        __syncthreads();
-    }
     if (wid == kIssuer) tc_dealloc(tmem, kTmemCols);
 }
 
