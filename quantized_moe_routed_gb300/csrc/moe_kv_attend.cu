@@ -6,8 +6,8 @@
 //
 // in one pass over the cache with a running maximum m and sum.  The cache's
 // bytes bound it: each page and kv head is read once for all query heads that
-// share it (a decode batch of ragged lengths, 1.1 GB of cache: 176 us, 94% of the
-// measured copy rate; one sequence of 4001 tokens: 10.9 us, its fixed costs).  The E4M3 codes become fp16 in registers (exact) for mma.sync
+// share it (a decode batch of ragged lengths, 1.1 GB of cache: 178 us, 93% of the
+// measured copy rate; one sequence of 4002 tokens: 11.1 us, its fixed costs).  The E4M3 codes become fp16 in registers (exact) for mma.sync
 // m16n8k16; q enters as fp16 after a power-of-two prescale of its row (exact
 // for elements down to 2^-28 of the row's largest), the weights as fp16 of 256 w vs (vs: the
 // page's v scale over the largest that the maximum allows for); their sum

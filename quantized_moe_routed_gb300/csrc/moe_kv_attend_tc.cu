@@ -34,10 +34,11 @@
 // and P V during the following softmax.  Only the reference goes from step to step, as
 // soon as a step's maxima are known.  Two threads bring pages, a warp issues the
 // products for S and one those for O, two pairs of warps convert v.  2048 new tokens after
-// 14336, 32 heads of 128 on 8: 449 us, 1300 TFLOP/s; a step takes 1920 cycles, of which
-// the tensor cores work 1024 and the exponentials 1024 a pair of warps; the rest are
-// waits between them.  (Commits for each page of P, turns for the exponentials,
-// four softmax warpgroups, an eighth of the exponentials as polynomials all measured
+// 16384, 32 heads of 128 on 8: 455 us, 1280 TFLOP/s; a step takes about 1900 cycles, of
+// which the tensor cores work 1024 and the exponentials 512; the rest are waits between
+// them.  (Before runs ended the chunk took 437 us: ending them costs 2, the code for it in
+// the loops the rest.  Measured against 449 then: commits for each page of P, turns for the
+// exponentials, four softmax warpgroups, an eighth of the exponentials as polynomials, all
 // slower: 484, 537, 524 and 476 us.)  With two row
 // tiles a block sharing k and v, tensor memory leaves no room for this (S and P in one
 // place): the softmax then waits for the chain from its weights over P V to the next

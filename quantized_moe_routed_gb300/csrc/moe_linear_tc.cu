@@ -13,10 +13,11 @@
 // block's rows over its tiles, not 128: every block brings the same number of bytes.
 //
 // 24 tokens, 65543 rows of 4096: 44.7 us, 52% of the rate at which memory could
-// bring the weights (66 us with mma.sync).  The conversion bounds it (two
-// instructions per pair of weights, 8 warps), then the pass over x that finds the
-// tokens' scales (every block reads all of x before its first product, 5 us) and the
-// products (43 cycles for each 128 x 16 of A, whatever the tokens).
+// bring the weights (66 us with mma.sync).  No unit is full (issue 51%, ALU 43%, DRAM
+// 38% in a profile): the eight converting warps' waits bound it, two warps a scheduler with
+// little to cover them (loads of codes, their stores to tensor memory, a free buffer, and
+// every 512 elements the end of the products, 4 us), then the pass over x that finds
+// the tokens' scales (every block reads all of x before its first product, 5 us).
 //
 // x enters as fp16 after a power-of-two scale of each token, from its largest
 // element and undone at the end: bf16's 8 bits are exact down to 2^-31 of the
