@@ -124,7 +124,7 @@ def _logits(g, case):
     T, V = case["T"], case["V"]
     x = torch.randn((T, V), generator=g, device=DEV) * (0.7 + 2 * torch.rand((T, 1), generator=g, device=DEV))
     m = min(V, 40)
-    at = torch.randint(0, V, (T, m), generator=g, device=DEV)
+    at = (torch.randint(0, V, (T, 1), generator=g, device=DEV) + torch.arange(m, device=DEV) * (V // m)) % V  # apart
     top = 12 * torch.exp(-torch.arange(m, device=DEV) / 8.0) * torch.rand((T, m), generator=g, device=DEV)
     x.scatter_(1, at, 4 + top)
     if case["masked"]:  # a grammar leaves a tenth of the tokens, one at least
