@@ -19,10 +19,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_nvfp4.so")
 SOURCES = ("moe_kernels.cu", "moe_tc.cu", "moe_small.cu", "moe_gemv.cu", "moe_route.cu", "moe_abi.cu",
            "moe_norm.cu", "moe_linear.cu", "moe_linear_tc.cu", "moe_kv_append.cu", "moe_kv_attend.cu", "moe_kv_attend_tc.cu",
-           "moe_layer.cu")
+           "moe_kv_move.cu", "moe_sample.cu", "moe_layer.cu", "moe_speculate.cu")
 HEADERS = ("moe_internal.h", "moe_device.cuh", "moe_tcgen05.cuh", "moe_host.h", "moe_layer_internal.h",
-           "moe_layer_device.cuh", "moe_attend.cuh", "moe_ring.h")
-ABI = ("moe_nvfp4.h", "moe_layer.h")
+           "moe_layer_device.cuh", "moe_layer_host.h", "moe_attend.cuh", "moe_ring.h")
+ABI = ("moe_nvfp4.h", "moe_layer.h", "moe_speculate.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,7 +52,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         cmd = [cc] + common + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if src not in ("moe_abi.cu", "moe_layer.cu"):
+        if src not in ("moe_abi.cu", "moe_layer.cu", "moe_speculate.cu"):
             cmd += ["-Xptxas", "-v"]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         objs.append(obj)

@@ -45,6 +45,35 @@ __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, co
 // Tokens that row r of a sequence sees (r = new token * group + head).
 __device__ __forceinline__ int row_sees(int len, int n, int G, int r) { return max(len - n + r / G + 1, 0); }
 
+// The tokens of W pages from pg on that new token i of a tree sees, a bit each: those
+// before the tree (the sequence's first `past`), those on the way from i to the root.  A
+// parent is an earlier token, so the way back ends; one that is not counts as a
+// root.  (The way is walked for each page that holds tokens of the tree: a few loads
+// that hit L1, against masks of all tokens kept for one or two steps.)
+template <int W>
+__device__ __forceinline__ void tree_sees(const AttendParams &p, int q0, int past, int i, int pg, uint64_t (&w)[W])
+{
+    const int base = pg * kPage - past;  // the tree's token in slot 0 of page pg
+#pragma unroll
+    for (int x = 0; x < W; ++x) {
+        const int b = base + x * kPage;
+        w[x] = b >= 0 ? 0ull : (b <= -kPage ? ~0ull : (1ull << -b) - 1ull);
+    }
+    const int first = max(base, 0);
+    while (i >= first) {
+        const int d = i - base;
+#pragma unroll
+        for (int x = 0; x < W; ++x)
+            if ((d >> 6) == x) w[x] |= 1ull << (d & 63);
+        const int up = __ldg(p.parent + q0 + i);
+        if (up >= i || up < -1) {
+            atomicOr(p.c.ctrl + 2, kErrBadIndex);
+            break;
+        }
+        i = up;
+    }
+}
+
 // Units of row tile j: COST, and its pages, or one where its last row sees
 // nothing (the tile's zeros still have to be written).
 template <int COST>
@@ -55,7 +84,7 @@ __device__ __forceinline__ int tile_units(int len, int n, int G, int TR, int j)
 }
 
 // Fill in the sequences and their units; all threads of the block.
-template <int COST>
+template <int COST, bool TREE>
 __device__ __forceinline__ void plan_units(const AttendParams &p, Seqs &sq, int G, int TR)
 {
     const KvParams &c = p.c;
@@ -63,7 +92,8 @@ __device__ __forceinline__ void plan_units(const AttendParams &p, Seqs &sq, int 
     for (int b = tid; b < c.B; b += blockDim.x) {
         const int a0 = c.q_off[b], a1 = c.q_off[b + 1], l = c.kv_len[b];
         const int q0 = min(max(a0, 0), c.N), q1 = min(max(a1, q0), c.N);
-        const int len = l < 0 || l > c.max_pages * kPage ? 0 : l;  // out of range: nothing is seen
+        // out of range, or too long for a tree: nothing is seen
+        const int len = l < 0 || l > c.max_pages * kPage || (TREE && q1 - q0 > MOE_KV_MAX_TREE) ? 0 : l;
         if (blockIdx.x == 0 && (q0 != a0 || q1 != a1 || len != l)) atomicOr(c.ctrl + 2, kErrBadIndex);
         sq.q0[b] = q0;
         sq.n[b] = q1 - q0;

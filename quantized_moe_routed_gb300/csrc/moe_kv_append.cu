@@ -158,18 +158,6 @@ __device__ __forceinline__ void block_max2(float &a, float &b, float *red)
     }
 }
 
-// Sixteen codes times f (a power of two, or a ratio of caller's scales).
-__device__ __forceinline__ uint4 requant16(uint4 w, float f)
-{
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = e4m3_unpack4(u4w(w, i));
-        o[i] = e4m3_pack4(v.x * f, v.y * f, v.z * f, v.w * f);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // The page's new scale from the new tokens' largest, and the factor of the
 // codes already there (1: they stay).
 __device__ __forceinline__ float new_scale(float amax, bool old_tokens, float old, float &factor)
@@ -185,7 +173,8 @@ __device__ __forceinline__ float new_scale(float amax, bool old_tokens, float ol
     return s;
 }
 
-template <int D, Rot ROT>
+// TREE: the new tokens are trees, turned by their depth behind the tokens before the tree.
+template <int D, Rot ROT, bool TREE>
 __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) moe_kv_append_kernel(const AppendParams p)
 {
     constexpr int UT = D / 16;            // units of a token
@@ -203,7 +192,8 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
     // the sequence, with offsets and lengths kept inside the step's arrays
     const int q0 = min(max(c.q_off[b], 0), c.N), q1 = min(max(c.q_off[b + 1], q0), c.N);
     const int n = q1 - q0, lens = c.kv_len[b];
-    const int len = lens < 0 || lens > c.max_pages * kPage ? 0 : lens;  // out of range: nothing has a position
+    // out of range, or too long for a tree: nothing has a position
+    const int len = lens < 0 || lens > c.max_pages * kPage || (TREE && n > MOE_KV_MAX_TREE) ? 0 : lens;
     const int first = len - n;  // position of the first new token
     if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0 &&
         (q0 != c.q_off[b] || q1 != c.q_off[b + 1] || first < 0 || len != lens))
@@ -234,6 +224,21 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
         r.turns = c.rot_dim == 0 || r.pos0 + r.cnt <= c.rope_positions;
         return r;
     };
+    // The position that turns the token stored at `at` (never behind it: inside the table if that is).
+    auto angle_at = [&](int at) {
+        if (!TREE || ROT == kNone) return at;
+        int depth = 0;
+        for (int i = at - first; i >= 0;) {  // (a parent is an earlier token, so this ends)
+            const int up = __ldg(p.parent + q0 + i);
+            if (up >= i || up < -1) {
+                atomicOr(c.ctrl + 2, kErrBadIndex);
+                break;
+            }
+            if (up >= 0) ++depth;
+            i = up;
+        }
+        return max(first + depth, 0);
+    };
     // (two loops: in one, what either kind of block needs would be held through the other's)
     if (queries) {
         for (int pg = page0 + blockIdx.x; pg * kPage < len; pg += gridDim.x) {
@@ -242,13 +247,14 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
             if (const int tok = tid / UT, u = tid % UT; tok < cnt) {
                 const Units<ROT> un(c, u);
                 float2 cs[8];
-                if (turns) load_angles<ROT>(c, cs, pos0 + tok, u);
+                const int pos = turns ? angle_at(pos0 + tok) : 0;
+                if (turns) load_angles<ROT>(c, cs, pos, u);
                 const uint16_t *src = p.q + (row0 + tok) * p.q_stride + h * G * D;
                 uint16_t *dst = p.q_out + (static_cast<size_t>(row0 + tok) * c.q_heads + h * G) * D;
 #pragma unroll 1
                 for (int g = 0; g < G; ++g) {
                     float v[16];
-                    if (turns) load_unit<ROT>(c, v, src + g * D, un, cs, pos0 + tok);
+                    if (turns) load_unit<ROT>(c, v, src + g * D, un, cs, pos);
                     // where partners are other elements of the token's UT lanes, all are read before
                     // any is written: the queries may be rotated in place
                     if (ROT == kOddHalves) __syncwarp(((1u << UT) - 1u) << (tid & 31 & ~(UT - 1)));
@@ -278,8 +284,9 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
             const uint4 *zp = reinterpret_cast<const uint4 *>(p.v + (row0 + tok) * p.v_stride + h * D + 16 * u);
             z[0] = zp[0];
             z[1] = zp[1];
-            load_angles<ROT>(c, cs, pos0 + tok, u);
-            load_unit<ROT>(c, x, p.k + (row0 + tok) * p.k_stride + h * D, un, cs, pos0 + tok);
+            const int pos = angle_at(pos0 + tok);
+            load_angles<ROT>(c, cs, pos, u);
+            load_unit<ROT>(c, x, p.k + (row0 + tok) * p.k_stride + h * D, un, cs, pos);
         }
         if (!turns || id < 0 || id >= c.n_pages) {
             if (tid == 0) atomicOr(c.ctrl + 2, kErrBadIndex);
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
     }
 }
 
-template <int D, Rot ROT>
+template <int D, Rot ROT, bool TREE>
 cudaError_t launch_one(const AppendParams &p, cudaStream_t st)
 {
     const KvParams &c = p.c;
@@ -372,22 +379,23 @@ cudaError_t launch_one(const AppendParams &p, cudaStream_t st)
     // given too small
     const int pages = std::min(std::max(c.max_q, 1) / kPage + 2, c.max_pages);
     LaunchCfg l(dim3(c.max_q <= 1 ? 1 : pages, c.B, c.kv_heads * (p.q ? 2 : 1)), dim3(kPage * D / 16), 0, st);
-    return cudaLaunchKernelEx(&l.cfg, moe_kv_append_kernel<D, ROT>, p);
+    return cudaLaunchKernelEx(&l.cfg, moe_kv_append_kernel<D, ROT, TREE>, p);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_d(const AppendParams &p, cudaStream_t st)
 {
-    if (p.c.rot_dim == 0) return launch_one<D, kNone>(p, st);
-    if (p.c.rot_inter) return launch_one<D, kNeighbours>(p, st);
-    return p.c.rot_dim % 16 == 0 ? launch_one<D, kHalves>(p, st) : launch_one<D, kOddHalves>(p, st);
+    if (p.c.rot_dim == 0) return launch_one<D, kNone, TREE>(p, st);
+    if (p.c.rot_inter) return launch_one<D, kNeighbours, TREE>(p, st);
+    return p.c.rot_dim % 16 == 0 ? launch_one<D, kHalves, TREE>(p, st) : launch_one<D, kOddHalves, TREE>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t st)
 {
-    return p.c.D == 128 ? launch_d<128>(p, st) : launch_d<64>(p, st);
+    if (p.parent) return p.c.D == 128 ? launch_d<128, true>(p, st) : launch_d<64, true>(p, st);
+    return p.c.D == 128 ? launch_d<128, false>(p, st) : launch_d<64, false>(p, st);
 }
 
 }  // namespace moe

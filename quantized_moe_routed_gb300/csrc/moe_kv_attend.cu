@@ -79,8 +79,9 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
 __host__ __device__ constexpr int merge_cols(int D, int NX) { return D < 64 / NX ? D : 64 / NX; }
 
 // NX: query rows of a tile / 8 (1 or 2).  Shared memory: ring of stages (k page,
-// v page), the control block, the sequences, the warps' results.
-template <int D, int NX>
+// v page), the control block, the sequences, the warps' results.  TREE: the new tokens
+// are trees, and see the way to their root instead of all before them.
+template <int D, int NX, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid_constant__ AttendParams p, int NS)
 {
     constexpr int TR = 8 * NX;                  // query rows of a tile
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
     }
     grid_wait();
     grid_release();
-    plan_units<kTileCost>(p, sq, G, TR);
+    plan_units<kTileCost, TREE>(p, sq, G, TR);
     const long long U = sq.cum[c.B];
     const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
     if (static_cast<int>(blockIdx.x) >= blocks) return;
@@ -198,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                     for (int i = 0; i < 2 * KS; ++i) qf[x][i] = 0u;
                 }
             }
-            const int tile_sees = row_sees(len, n, G, s.tile * TR);  // the tile's first row sees the least
+            // the tile's first row sees the least; of a tree's tokens each sees what is before the tree
+            const int tile_sees = TREE ? max(len - n, 0) : row_sees(len, n, G, s.tile * TR);
 
             float m[NX], l[NX];
 #pragma unroll
@@ -254,17 +256,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 const bool edge = (pg + 1) * kPage > tile_sees;
                 const float lv = scale_log2(vs), pv = vs * 256.f;
                 float fs[NX], mx[NX];
+                uint64_t see[NX];  // TREE: the page's tokens that a row sees, the lane's first lowest
 #pragma unroll
                 for (int x = 0; x < NX; ++x) {
                     fs[x] = qs[x] * ks;
                     mx[x] = -INFINITY;
+                    see[x] = 0ull;
+                    if (TREE && edge) {
+                        uint64_t w[1] = {0ull};
+                        const int r = s.tile * TR + 8 * x + g;
+                        if (r < rows) tree_sees<1>(p, q0, len - n, r / G, pg, w);
+                        see[x] = w[0] >> (16 * t4 + 2 * NJ * half);
+                    }
                 }
+                if (TREE) __syncwarp();
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int x = 0; x < 2 * NX; ++x) {
                         sc[j][x] *= fs[x >> 1];
-                        if (edge && pg * kPage + 16 * t4 + 2 * (NJ * half + j) + (x & 1) >= sees[x >> 1]) sc[j][x] = -INFINITY;
+                        if (edge && (TREE ? !((see[x >> 1] >> (2 * j + (x & 1))) & 1ull)
+                                          : pg * kPage + 16 * t4 + 2 * (NJ * half + j) + (x & 1) >= sees[x >> 1]))
+                            sc[j][x] = -INFINITY;
                         mx[x >> 1] = fmaxf(mx[x >> 1], sc[j][x]);
                     }
                 float ref[NX], alpha[NX];
@@ -395,27 +408,36 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
     }
 }
 
-template <int D, int NX>
+template <int D, int NX, bool TREE>
 cudaError_t launch_one(const AttendParams &p, int grid, int smem_optin, cudaStream_t st)
 {
     constexpr int kStage = 2 * kPage * D;
     const int fixed = 1024 + static_cast<int>(sizeof(Control) + sizeof(Seqs)) + kWarps * 8 * NX * (merge_cols(D, NX) + 6) * 4;
     const int ns = std::min(kMaxStages, (smem_optin - fixed) / kStage) / kGroups * kGroups;
     const int smem = fixed + ns * kStage;
-    auto *fn = moe_kv_attend_kernel<D, NX>;
+    auto *fn = moe_kv_attend_kernel<D, NX, TREE>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     LaunchCfg l(dim3(grid), dim3(kThreads), smem, st);
     return cudaLaunchKernelEx(&l.cfg, fn, p, ns);
 }
 
+template <bool TREE>
+cudaError_t launch_rows(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st)
+{
+    if (p.c.D == 128)
+        return tile_rows == 8 ? launch_one<128, 1, TREE>(p, num_sms, smem_optin, st)
+                              : launch_one<128, 2, TREE>(p, num_sms, smem_optin, st);
+    return tile_rows == 8 ? launch_one<64, 1, TREE>(p, num_sms, smem_optin, st)
+                          : launch_one<64, 2, TREE>(p, num_sms, smem_optin, st);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_attend_rows(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st)
 {
-    if (p.c.D == 128)
-        return tile_rows == 8 ? launch_one<128, 1>(p, num_sms, smem_optin, st) : launch_one<128, 2>(p, num_sms, smem_optin, st);
-    return tile_rows == 8 ? launch_one<64, 1>(p, num_sms, smem_optin, st) : launch_one<64, 2>(p, num_sms, smem_optin, st);
+    return p.parent ? launch_rows<true>(p, tile_rows, num_sms, smem_optin, st)
+                    : launch_rows<false>(p, tile_rows, num_sms, smem_optin, st);
 }
 
 }  // namespace moe

@@ -242,7 +242,8 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
     return d;
 }
 
-template <int D>
+// TREE: the new tokens are trees, and see the way to their root instead of all before them.
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __grid_constant__ AttendParams p)
 {
     constexpr int TR = kRows;
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     const uint32_t tmem = ct->tmem;
     grid_wait();
     grid_release();
-    plan_units<kTileCost>(p, sq, G, TR);
+    plan_units<kTileCost, TREE>(p, sq, G, TR);
     const long long U = sq.cum[c.B];
     const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
     if (static_cast<int>(blockIdx.x) >= blocks) {
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
             const int r = row0 + row;
             const int sees = r < rows ? row_sees(len, n, G, r) : 0;
             const float qs = steps > 0 && sees > 0 ? ct->qs[row] : 0.f;
-            const int tile_sees = row_sees(len, n, G, row0);  // the least of the tile's rows
+            const int tile_sees = TREE ? max(len - n, 0) : row_sees(len, n, G, row0);  // the least of the tile's rows
 
             float l = 0.f, lref = -INFINITY;  // this warpgroup's sum and what it refers to
             // (a run's end is a step of the segment's first warpgroup)
@@ -531,7 +532,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
                 tc_wait_ld();
                 tc_fence_before();
                 mbar_arrive(&ct->s_read[w]);
-                if (none0 || none1 || (pg + 2) * kPage > tile_sees) {
+                if (TREE) {
+                    if (none0 || none1 || (pg + 2) * kPage > tile_sees) {
+                        uint64_t see[2] = {0ull, 0ull};
+                        if (r < rows) tree_sees<2>(p, q0, len - n, r / G, pg, see);
+                        if (none0) see[0] = 0ull;
+                        if (none1) see[1] = 0ull;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const uint32_t bits = static_cast<uint32_t>(see[h >> 1] >> (32 * (h & 1)));
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!((bits >> j) & 1u)) a[h][j] = -INFINITY;
+                        }
+                    }
+                    __syncwarp();
+                } else if (none0 || none1 || (pg + 2) * kPage > tile_sees) {
                     const int lim0 = none0 ? 0 : sees - pg * kPage, lim1 = none1 ? 0 : sees - (pg + 1) * kPage;
 #pragma unroll
                     for (int h = 0; h < 4; ++h)
@@ -711,14 +727,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_tc_kernel(const __g
     if (wid == kIssuer) tc_dealloc(tmem, kTmemCols);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_d(const AttendParams &p, int grid, cudaStream_t st)
 {
     // steps of k, of v, of v in fp16 (twice as many bytes), query digits
     constexpr int smem = 1024 + 2 * kPage * D * (kKStages + kVStages + 2 * kFStages) + 2 * kRows * D +
                          static_cast<int>(sizeof(Control) + sizeof(Seqs));
     static_assert(smem <= 227 * 1024, "shared memory of a block");
-    auto *fn = moe_kv_attend_tc_kernel<D>;
+    auto *fn = moe_kv_attend_tc_kernel<D, TREE>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     LaunchCfg l(dim3(grid), dim3(kThreads), smem, st);
@@ -729,7 +745,8 @@ cudaError_t launch_d(const AttendParams &p, int grid, cudaStream_t st)
 
 cudaError_t launch_kv_attend_tc(const AttendParams &p, int num_sms, cudaStream_t st)
 {
-    return p.c.D == 128 ? launch_d<128>(p, num_sms, st) : launch_d<64>(p, num_sms, st);
+    if (p.parent) return p.c.D == 128 ? launch_d<128, true>(p, num_sms, st) : launch_d<64, true>(p, num_sms, st);
+    return p.c.D == 128 ? launch_d<128, false>(p, num_sms, st) : launch_d<64, false>(p, num_sms, st);
 }
 
 }  // namespace moe

@@ -41,6 +41,18 @@ __device__ __forceinline__ float4 e4m3_unpack4(uint32_t w)
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// Sixteen codes times f (a power of two, or a ratio of caller's scales).
+__device__ __forceinline__ uint4 requant16(uint4 w, float f)
+{
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = e4m3_unpack4(u4w(w, i));
+        o[i] = e4m3_pack4(v.x * f, v.y * f, v.z * f, v.w * f);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Exponent e of the smallest power of two with a <= 448 * 2^e, at least -64
 // (a >= 0, finite).  448 = 1.75 * 2^8, so with a = m * 2^E it is E - 8, or
 // E - 7 where m > 1.75.

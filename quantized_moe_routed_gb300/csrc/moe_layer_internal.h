@@ -1,7 +1,8 @@
-// moe_layer_internal.h -- launch interface between the host side of the layer
-// operators (moe_layer.cu) and their kernels.  Not part of the ABI.
+// moe_layer_internal.h -- launch interface between the host sides of the layer operators
+// (moe_layer.cu, moe_speculate.cu) and their kernels.  Not part of the ABI.
 #pragma once
 #include "moe_layer.h"
+#include "moe_speculate.h"
 
 #include <cstddef>
 #include <cstdint>
@@ -70,6 +71,7 @@ struct AppendParams {
     const uint16_t *q, *k, *v;
     long long q_stride, k_stride, v_stride;
     uint16_t *q_out;
+    const int32_t *parent = nullptr;  // the new tokens are trees (moe_speculate.h): [N], else null
 };
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t st);
 
@@ -83,11 +85,31 @@ struct AttendParams {
     uint32_t *count;    // [grid] arrivals at the tiles that start in a CTA and end in a later one
     float *part;        // [2 * grid] partial results (attend_part_floats each)
     long long timeout_ns;
+    const int32_t *parent = nullptr;  // as in AppendParams
 };
 constexpr int kAttendMaxRows = 128;  // query rows of the largest tile
 __host__ __device__ inline size_t attend_part_floats(int D) { return static_cast<size_t>(kAttendMaxRows) * (D + 2); }
 cudaError_t launch_kv_attend_rows(const AttendParams &p, int tile_rows, int num_sms, int smem_optin, cudaStream_t st);
 // moe_kv_attend_tc.cu: tiles of 128 rows
 cudaError_t launch_kv_attend_tc(const AttendParams &p, int num_sms, cudaStream_t st);
+
+// moe_kv_move.cu
+struct CompactParams {
+    KvParams c;
+    const int32_t *keep, *n_keep;
+    int max_keep;
+    int32_t *kv_len_out;
+};
+cudaError_t launch_kv_compact(const CompactParams &p, cudaStream_t st);
+struct ForkParams {
+    KvParams c;  // kv_len, pages, max_pages, B: the sequences that children go on from
+    const int32_t *src, *fresh;
+    int C;
+    int32_t *kv_len_out, *pages_out;
+};
+cudaError_t launch_kv_fork(const ForkParams &p, cudaStream_t st);
+
+// moe_sample.cu
+cudaError_t launch_sample(const moe_sample_desc &d, cudaStream_t st);
 
 }  // namespace moe

@@ -1,7 +1,10 @@
 """The operators around the routed experts in a decoder layer (the C ABI in
 include/moe_layer.h): residual addition with root-mean-square norm, projections
 with NVFP4 weights, the paged 8-bit key/value cache with its append (rotation
-included) and the attention over it.
+included) and the attention over it; and what speculative decoding and several samples
+of a prompt ask of them (include/moe_speculate.h): trees of new tokens, the compaction
+of the cache to the accepted ones, the fork of sequences, the sampling of tokens
+from logits.
 
 Argument marshalling only, as in `binding`: every step of the computation runs
 in the library's sm_103a kernels, on `stream` or the current stream; outputs
@@ -21,6 +24,8 @@ from .binding import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _need
 
 PAGE = 64        # tokens of a cache page
 MAX_SEQS = 512   # sequences of a step
+MAX_TREE = 256   # new tokens of a sequence that are a tree
+MAX_VOCAB = 262144  # logits of a row that tokens are sampled from
 _BF16 = (torch.bfloat16,)
 
 _P, _I, _S, _L, _F = C.c_void_p, C.c_int, C.c_size_t, C.c_int64, C.c_float
@@ -37,6 +42,12 @@ class moe_kv_batch(C.Structure):
                 ("max_q", _I)]
 
 
+class moe_sample_desc(C.Structure):
+    _fields_ = [("logits_dev", _P), ("stride", _L), ("bf16", _I), ("T", _I), ("V", _I), ("u_dev", _P),
+                ("temperature_dev", _P), ("temperature", _F), ("top_k_dev", _P), ("top_k", _I), ("top_p_dev", _P),
+                ("top_p", _F), ("min_p_dev", _P), ("min_p", _F), ("token_dev", _P), ("prob_dev", _P)]
+
+
 # Every function include/moe_layer.h declares: name -> (restype, argtypes).
 SIGNATURES = {
     "moe_norm": (_I, [_P, _I, _L, _P, _P, _P, _F, _P, _P, _P, _I, _I, _P]),
@@ -49,15 +60,23 @@ SIGNATURES = {
     "moe_kv_attend": (_I, [_P, _P, _L, _F, _P, C.POINTER(moe_kv_batch), _P, _P]),
     "moe_kv_check": (_I, [_P, _P, _P]),
 }
+# And include/moe_speculate.h.
+SPECULATE_SIGNATURES = {
+    "moe_kv_append_tree": (_I, [_P, _P, _L, _P, _L, _P, _L, _P, C.POINTER(moe_kv_batch), _P, _P, _P]),
+    "moe_kv_attend_tree": (_I, [_P, _P, _L, _F, _P, C.POINTER(moe_kv_batch), _P, _P, _P]),
+    "moe_kv_compact": (_I, [_P, _P, _P, _I, _P, C.POINTER(moe_kv_batch), _P, _P]),
+    "moe_kv_fork": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P]),
+    "moe_sample": (_I, [C.POINTER(moe_sample_desc), _P]),
+}
 _ready = None
 
 
 def _library():
-    """The library, with this header's functions prototyped."""
+    """The library, with both headers' functions prototyped."""
     global _ready
     lib = binding.load_library()
     if _ready is not lib:
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **SPECULATE_SIGNATURES}.items():
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
         _ready = lib
@@ -312,12 +331,15 @@ class KVCache:
             _same_device(self.device, ws=ws)
             raise _bad("ws is smaller than this cache's workspace (new_workspace)")
 
-    def append(self, k, v, q_off, kv_len, pages, ws, max_q: int, q=None, q_out=None, stream=None):
+    def append(self, k, v, q_off, kv_len, pages, ws, max_q: int, q=None, q_out=None, stream=None, parents=None):
         """Rotate and append the new tokens' k and v (bfloat16 [N, kv_heads,
         head_dim], tokens may be strided), and rotate q (bfloat16 [N, q_heads,
         head_dim]) into q_out, which is returned (None without q) and may be q.
         Rows outside every sequence (before q_off[0], from q_off[B] on) are not
-        read and not written: a q_out allocated here holds anything there."""
+        read and not written: a q_out allocated here holds anything there.  parents
+        (int32 [N]) makes each sequence's new tokens a tree of up to MAX_TREE: the token
+        before each, counted inside the sequence's new ones, or -1 at a root; a token
+        turns by its depth (moe_kv_append_tree), and is stored in the order given."""
         dev = self.device
         ks = _rows(k, _BF16, self._kv_row, "k")
         N = k.shape[0]
@@ -336,19 +358,25 @@ class KVCache:
                 _need_out(q_out, torch.bfloat16, (N, *self._q_row), dev, "q_out")
         elif q_out is not None:
             raise _bad("q_out without q")
-        st = _library().moe_kv_append(self.handle, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_out),
-                                      self._step(q_off, kv_len, pages, ws, N, max_q), ws.data_ptr(), handle)
+        args = (self.handle, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_out),
+                self._step(q_off, kv_len, pages, ws, N, max_q))
+        if parents is None:
+            st = _library().moe_kv_append(*args, ws.data_ptr(), handle)
+        else:
+            self._need_int32(parents, (N,), "parents")
+            st = _library().moe_kv_append_tree(*args, parents.data_ptr(), ws.data_ptr(), handle)
         if st != MOE_OK:
             _check(st)
         return q_out
 
-    def attend(self, q, q_off, kv_len, pages, ws, max_q: int, scale: float = None, out=None, stream=None):
+    def attend(self, q, q_off, kv_len, pages, ws, max_q: int, scale: float = None, out=None, stream=None, parents=None):
         """Causal attention of q (bfloat16 [N, q_heads, head_dim], tokens may be
         strided) over the cache: bfloat16 [N, q_heads, head_dim].  scale: 1 /
         sqrt(head_dim) unless given.  A token that sees nothing gets 0; rows
         outside every sequence (before q_off[0], from q_off[B] on) are not written:
         an out allocated here holds anything there, so give a zeroed one where
-        what follows reads padded rows."""
+        what follows reads padded rows.  parents as in append: a token then sees the
+        tokens before the tree and the way to its root (moe_kv_attend_tree)."""
         dev = self.device
         qs = _rows(q, _BF16, self._q_row, "q")
         if q.device != dev:
@@ -358,14 +386,123 @@ class KVCache:
             out = _empty(q.shape, torch.bfloat16, dev, stream)
         else:
             _need_out(out, torch.bfloat16, q.shape, dev, "out")
-        st = _library().moe_kv_attend(self.handle, q.data_ptr(), qs, self._scale if scale is None else scale,
-                                      out.data_ptr(), self._step(q_off, kv_len, pages, ws, q.shape[0], max_q),
-                                      ws.data_ptr(), handle)
+        args = (self.handle, q.data_ptr(), qs, self._scale if scale is None else scale, out.data_ptr(),
+                self._step(q_off, kv_len, pages, ws, q.shape[0], max_q))
+        if parents is None:
+            st = _library().moe_kv_attend(*args, ws.data_ptr(), handle)
+        else:
+            self._need_int32(parents, (q.shape[0],), "parents")
+            st = _library().moe_kv_attend_tree(*args, parents.data_ptr(), ws.data_ptr(), handle)
         if st != MOE_OK:
             _check(st)
         return out
+
+    def compact(self, keep, n_keep, q_off, kv_len, pages, ws, max_q: int, kv_len_out=None, stream=None):
+        """Keep the accepted ones of each sequence's newest tokens (moe_kv_compact),
+        those that a step appended with the same q_off, kv_len and pages: of sequence
+        b's n the ones keep[b, :n_keep[b]] (int32 [B, K], ascending; n_keep int32 [B]),
+        which move up to follow the tokens before them.  Returns the new lengths, int32
+        [B]; kv_len is left as it is (and kv_len_out is another array)."""
+        dev = self.device
+        handle = _handle(stream, dev)
+        step = self._step(q_off, kv_len, pages, ws, (1 << 30) // self.q_heads, max_q)
+        B = kv_len.shape[0]
+        if not isinstance(keep, torch.Tensor) or keep.dim() != 2:
+            raise _bad("keep must be a CUDA tensor [B, K]")
+        K = keep.shape[1]
+        self._need_int32(keep, (B, K), "keep")
+        self._need_int32(n_keep, (B,), "n_keep")
+        if kv_len_out is None:
+            kv_len_out = _empty((B,), torch.int32, dev, stream)
+        else:
+            self._need_int32(kv_len_out, (B,), "kv_len_out")
+        st = _library().moe_kv_compact(self.handle, keep.data_ptr(), n_keep.data_ptr(), K, kv_len_out.data_ptr(), step,
+                                       ws.data_ptr(), handle)
+        if st != MOE_OK:
+            _check(st)
+        return kv_len_out
+
+    def fork(self, src, fresh, kv_len, pages, ws, pages_out=None, kv_len_out=None, stream=None):
+        """Sequences that go on from others (moe_kv_fork): child c has the tokens of
+        sequence src[c] (int32 [C]) of kv_len [B] and pages [B, max_pages].  fresh[c]
+        (int32 [C]) is a free page that becomes the child's own for the tokens to come,
+        with a copy of what the sequence's last page holds; -1 leaves the child the
+        sequence's own page (for one child at most).  Full pages are shared.
+        Returns (pages, kv_len) of the children, int32 [C, max_pages] and [C]."""
+        dev = self.device
+        handle = _handle(stream, dev)
+        B = kv_len.shape[0] if isinstance(kv_len, torch.Tensor) and kv_len.dim() == 1 else -1
+        width = pages.shape[1] if isinstance(pages, torch.Tensor) and pages.dim() == 2 else -1
+        C_ = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
+        self._need_int32(kv_len, (B,), "kv_len")
+        self._need_int32(pages, (B, width), "pages")
+        self._need_int32(src, (C_,), "src")
+        self._need_int32(fresh, (C_,), "fresh")
+        self._need_ws(ws)
+        if pages_out is None:
+            pages_out = _empty((C_, width), torch.int32, dev, stream)
+        else:
+            self._need_int32(pages_out, (C_, width), "pages_out")
+        if kv_len_out is None:
+            kv_len_out = _empty((C_,), torch.int32, dev, stream)
+        else:
+            self._need_int32(kv_len_out, (C_,), "kv_len_out")
+        st = _library().moe_kv_fork(self.handle, src.data_ptr(), fresh.data_ptr(), C_, kv_len.data_ptr(), pages.data_ptr(),
+                                    width, B, kv_len_out.data_ptr(), pages_out.data_ptr(), ws.data_ptr(), handle)
+        if st != MOE_OK:
+            _check(st)
+        return pages_out, kv_len_out
+
+    def _need_int32(self, t, shape, name):
+        if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == self.device and t.shape == shape and
+                t.is_contiguous()):
+            _need(t, torch.int32, name)
+            _same_device(self.device, **{name: t})
+            raise _bad(f"{name} {tuple(t.shape)} is not {shape}")
 
     def check(self, ws, stream=None) -> int:
         """Synchronise and return the device status (0 = MOE_OK); clears it."""
         self._need_ws(ws)
         return int(_library().moe_kv_check(self.handle, ws.data_ptr(), _handle(stream, self.device)))
+
+
+def _setting(v, dtype, T, device, name):
+    """(device pointer, value) of a setting of the sampling: a tensor [T], or a number for all rows."""
+    if isinstance(v, torch.Tensor):
+        _need_out(v, dtype, (T,), device, name)
+        return v.data_ptr(), 0
+    return None, v
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=None, return_prob: bool = False,
+           stream=None):
+    """A token for each row of logits (float32 or bfloat16 [T, V], rows may be
+    strided), by the random numbers u (float32 [T], in [0, 1)): int32 [T]
+    (moe_sample).  temperature, top_p and min_p are numbers or float32 [T], top_k a
+    number or int32 [T]; temperature 0 gives the token of the largest logit, top_k 0,
+    top_p 1 and min_p 0 set no limit.  A row of -inf gives -1.  With return_prob (or
+    prob, float32 [T], to write to): (tokens, the probability that each was chosen with)."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise _bad("logits must be a CUDA tensor [T, V]")
+    T, V = logits.shape
+    stride = _rows(logits, (torch.float32, torch.bfloat16), (V,), "logits")
+    dev = logits.device
+    handle = _handle(stream, dev)
+    _need_out(u, torch.float32, (T,), dev, "u")
+    f32 = torch.float32
+    settings = (*_setting(temperature, f32, T, dev, "temperature"), *_setting(top_k, torch.int32, T, dev, "top_k"),
+                *_setting(top_p, f32, T, dev, "top_p"), *_setting(min_p, f32, T, dev, "min_p"))
+    if out is None:
+        out = _empty((T,), torch.int32, dev, stream)
+    else:
+        _need_out(out, torch.int32, (T,), dev, "out")
+    if prob is not None:
+        _need_out(prob, f32, (T,), dev, "prob")
+    elif return_prob:
+        prob = _empty((T,), f32, dev, stream)
+    d = moe_sample_desc(logits.data_ptr(), stride, logits.dtype == torch.bfloat16, T, V, u.data_ptr(), *settings,
+                        out.data_ptr(), _ptr(prob))
+    st = _library().moe_sample(C.byref(d), handle)
+    if st != MOE_OK:
+        _check(st)
+    return out if prob is None else (out, prob)
