@@ -110,6 +110,6 @@ struct ForkParams {
 cudaError_t launch_kv_fork(const ForkParams &p, cudaStream_t st);
 
 // moe_sample.cu
-cudaError_t launch_sample(const moe_sample_desc &d, cudaStream_t st);
+cudaError_t launch_sample(const moe_sample_desc &d, int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -6,7 +6,7 @@
 //
 // All three are one question: the first token, in order, at which a sum over the order
 // reaches a target, so no sort is needed.  Tokens are dealt into bins that keep the
-// order (2048 equal parts of the logits' range), a bin's tokens are counted and their
+// order (1024 equal parts of the logits' range), a bin's tokens are counted and their
 // weights added up, a scan over the bins finds the target's, and only that bin's
 // tokens (or all up to it, where those are few) are looked at one by one.
 //
@@ -14,19 +14,28 @@
 // them fit 64 bits): sums do not depend on the order of additions, so atomics give
 // the same bits every run, and borders are compared exactly.  A weight is
 // 2^-x, x = (max - l) log2(e) / t in two floats: 2^-(j / 64) from a table, the rest, below
-// 1/128, by its series; off by 2^-36 of itself.  (fp32 would be off by 2^-24, and one
-// row in a thousand would get another token than the formula says.)
+// 1/128, by its series; off by 2^-36 of itself, and from 2^-16 down, where most tokens are,
+// by half a unit (in 32 bits).  (fp32 would be off by 2^-24, and one row in a thousand
+// would get another token than the formula says.)
 //
-// A row belongs to a cluster of blocks, each with a part of the row in shared
-// memory, so that logits are read once; the blocks add up their bins through
-// distributed shared memory and the first one decides.
+// A row belongs to a cluster of blocks, each with a part of it; the blocks add up their
+// bins through distributed shared memory and the first one decides: it puts questions
+// (a range's places, finer bins of it, its tokens), which all answer.  16-bit logits are
+// counted by their value first, of which there are few, where a block has many: each
+// value is weighed once.
+//
+// Few rows are bound by latency: one of 65543 fp32 logits takes 21 us with top-k and top-p, of which the
+// weights take 5, adding up the bins 3, the list 4, each further target 1.5 (a barrier of the
+// cluster takes 0.5, a pass over the 8 blocks' parts 3); 24 such rows 37 us.  Many rows are
+// bound by the integer units (80 operations a weight, 45 a small one), 16-bit ones by the
+// shared memory's atomics (8 cycles for a warp's): 256 rows of 131075 take 279 us in fp32, 90 us in bf16
+// (205 us with every token weighed), 1.7 turns of a row an SM.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cstdint>
 
 namespace moe {
@@ -36,13 +45,13 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048, kPer = kBins / kThreads;  // bins of a pass over a row; of a thread
-constexpr int kList = 2048;                           // tokens that are looked at one by one
-constexpr int kFew = 32;                              // tokens that one warp orders
+constexpr int kMaxWarps = 32;
+constexpr int kBinBits = 10, kBins = 1 << kBinBits;  // bins of a pass over a row
+constexpr int kList = 2048;       // tokens that are looked at one by one
+constexpr int kFew = 32;          // tokens that one warp orders
 constexpr int kMaxCluster = 8;
-constexpr int kOne = 45;                              // a weight of 1 is 2^45
+constexpr int kOne = 45;          // a weight of 1 is 2^45
+constexpr int kCounters = 65536;  // of 16-bit logits by their bits, two to a word
 constexpr float kGreedy = 1e-6f;
 
 // A token's place in the order: its bin, its logit as an integer (larger logits
@@ -70,23 +79,25 @@ constexpr Powers make_powers()
 }
 __device__ const Powers kPowers = make_powers();
 
-struct Control {
-    u64 klo, khi;                  // what the cluster is asked to look at
-    int op, shift;
-    u64 mn, mx;                    // smallest and largest place in range (first: best order and index, last order)
-    int n;                         // tokens in the list
-    u64 powers[64];
-    u64 scan_w[kWarps];
-    uint32_t scan_n[kWarps];
-    u64 red[2 * kWarps];
-    // a target's bin, or its token
-    int bin;
-    u64 base_w, key_found, w_found;
-    uint32_t base_n, bin_n;
-    int few;
-    int small[kFew];
-};
+// What the first block asks of all: the smallest and largest place in [klo, khi]; bins of
+// 2^shift places from klo on; a list of the tokens in [klo, khi].
 enum Op { kDone, kRange, kHist, kGather };
+
+struct Control {
+    u64 best[kMaxCluster], last[kMaxCluster];  // of each block: smallest and largest place (first: order) in range
+    int ns[kMaxCluster];           // of each block: tokens in its list
+    u64 klo, khi;                  // the question, and kRange's answer
+    int op, shift;
+    int n, all;                    // tokens in the list, tokens that were meant to be
+    u64 powers[64];                // 2^(-j / 64) in units of 2^-61
+    int powers32[64];              // and of 2^-30
+    u64 scan_w[kMaxWarps], red[2 * kMaxWarps];
+    uint32_t scan_n[kMaxWarps];
+    int bin;                       // where a target lies: the bin, its tokens, the sums before it
+    uint32_t base_n, bin_n;
+    u64 base_w, key_found, w_found;
+    int few, small[kFew];
+};
 
 // ---- cluster
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -95,11 +106,23 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// In two halves around a kernel's start: no block's shared memory is touched from
+// another before that one runs.
+__device__ __forceinline__ void cluster_arrive()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // All threads of the cluster, and what they wrote to any block's shared memory.
 __device__ __forceinline__ void cluster_sync()
 {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // The address of p (in this block's shared memory) in block r's.
 __device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t r)
@@ -121,6 +144,15 @@ __device__ __forceinline__ u64 remote64(const void *p, uint32_t r)
     return v;
 }
 
+__device__ __forceinline__ void put32(const void *p, uint32_t r, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(p, r)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void put64(const void *p, uint32_t r, u64 v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_rank(p, r)), "l"(v) : "memory");
+}
+
 // ---- a row's settings and what its tokens weigh
 struct Row {
     float max, ch, cl, bins;  // 1 / t in units of log2(e), two floats; bins for a unit of x
@@ -128,15 +160,11 @@ struct Row {
     u64 least;                // min-p's least weight (1: any)
 };
 
-// A logit as it counts: NaN as -infinity, -0 as 0.
-__device__ __forceinline__ float clean(float l) { return l == l ? l + 0.f : -INFINITY; }
-__device__ __forceinline__ float counted(const Row &r, float l)
-{
-    return r.infinite ? (l == INFINITY ? 0.f : -INFINITY) : l;
-}
+// A logit as it counts in a row whose largest is +infinity.
+__device__ __forceinline__ float as_infinite(float l) { return l == INFINITY ? 0.f : -INFINITY; }
 __device__ __forceinline__ uint32_t order_of(float l)
 {
-    const uint32_t u = __float_as_uint(l);
+    const uint32_t u = __float_as_uint(l + 0.f);  // (-0 is 0)
     return ~(u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u));
 }
 __device__ __forceinline__ float logit_of(uint32_t order)
@@ -145,37 +173,66 @@ __device__ __forceinline__ float logit_of(uint32_t order)
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 
+// The functions of a token's weight and place are worked out in several places and
+// have to give the same everywhere: every operation says how it rounds.
+
 // x = (max - l) log2(e) / t as p + e.  p falls as l grows (every step of it rounds).
 __device__ __forceinline__ void exponent(const Row &r, float l, float &p, float &e)
 {
-    const float d = r.max - l, bb = d - r.max;
-    const float dl = (r.max - (d - bb)) + (-l - bb);  // d + dl = max - l
-    p = d * r.ch;
-    e = fmaf(d, r.ch, -p) + fmaf(d, r.cl, dl * r.ch);
+    const float d = __fsub_rn(r.max, l), bb = __fsub_rn(d, r.max);
+    const float dl = __fsub_rn(__fsub_rn(r.max, __fsub_rn(d, bb)), __fadd_rn(l, bb));  // d + dl = max - l
+    p = __fmul_rn(d, r.ch);
+    e = __fadd_rn(__fmaf_rn(d, r.ch, -p), __fmaf_rn(d, r.cl, __fmul_rn(dl, r.ch)));
 }
-constexpr float kNone = 46.5f;  // 2^-46.5 rounds to nothing
+constexpr float kNone = 46.5f;   // 2^-46.5 rounds to nothing
+constexpr float kSmall = 16.f;   // from here on 32 bits are enough
+constexpr float kMagic = 12582912.f;        // 1.5 * 2^23: adding it leaves the nearest whole number in the low bits,
+constexpr int kMagicBits = 0x4B400000;      // above these
 
-// 2^-(p + e) in units of 2^-45.
-__device__ __forceinline__ u64 weight(const u64 *powers, float p, float e)
+// 2^-(p + e) in units of 2^-45, kSmall <= p < kNone (0 for another p).
+__device__ __forceinline__ uint32_t small_weight(const Control *ct, float p, float e)
 {
-    if (!(p < kNone)) return 0ull;
-    const float kf = fmaf(p, 64.f, 12582912.f);  // the nearest whole number, in the low bits
-    const int j = __float_as_int(kf) - 0x4B400000;
-    const float r = fmaf(kf - 12582912.f, -1.f / 64.f, p);
-    // 2^-(r + e) - 1 = s - y - ye
-    const float y = r * 0.693147182f, ye = fmaf(r, 0.693147182f, -y) + fmaf(r, -1.90465421e-9f, e * 0.693147182f);
-    const float z = y + ye, s = z * z * (0.5f - z * (1.f / 6.f - z * (1.f / 24.f)));
-    const int dq = __float2int_rn(y * -274877906944.f) + __float2int_rn((s - ye) * 274877906944.f);  // in units of 2^-38
-    const u64 t = powers[j & 63];
-    const u64 w = t + static_cast<u64>((static_cast<long long>(static_cast<int>(t >> 31)) * dq) >> 7);
-    const int n = (61 - kOne) + (j >> 6);
-    return (w + (1ull << (n - 1))) >> n;
+    const bool in = p >= kSmall && p < kNone;
+    if (!in) p = kSmall, e = 0.f;
+    const float kf = __fmaf_rn(p, 64.f, kMagic);
+    const int j = __float_as_int(kf) - kMagicBits;
+    const float r = __fmaf_rn(__fsub_rn(kf, kMagic), -1.f / 64.f, p);
+    const float z = __fmul_rn(__fadd_rn(r, e), 0.693147182f);
+    // 2^-(r + e) - 1 = z^2 (1 / 2 - z / 6) - z
+    const float s = __fmaf_rn(__fmul_rn(z, z), __fmaf_rn(z, -1.f / 6.f, 0.5f), -z);
+    const int dq = __float2int_rn(__fmul_rn(s, 4294967296.f));
+    const int t = ct->powers32[j & 63];
+    const uint32_t w = static_cast<uint32_t>(t + __mulhi(t, dq));
+    const int n = (j >> 6) - (kOne - 30);
+    return in ? ((w >> (n - 1)) + 1u) >> 1 : 0u;
 }
+
+// The same for any p.
+__device__ __forceinline__ u64 weight(const Control *ct, float p, float e)
+{
+    if (p >= kSmall) return small_weight(ct, p, e);
+    if (!(p < kSmall)) return 0ull;
+    const float kf = __fmaf_rn(p, 64.f, kMagic);
+    const int j = __float_as_int(kf) - kMagicBits;
+    const float r = __fmaf_rn(__fsub_rn(kf, kMagic), -1.f / 64.f, p);
+    // 2^-(r + e) - 1 = s - y - ye
+    const float y = __fmul_rn(r, 0.693147182f);
+    const float ye = __fadd_rn(__fmaf_rn(r, 0.693147182f, -y), __fmaf_rn(r, -1.90465421e-9f, __fmul_rn(e, 0.693147182f)));
+    const float z = __fadd_rn(y, ye);
+    const float s = __fmul_rn(__fmul_rn(z, z), __fmaf_rn(z, -__fmaf_rn(z, -1.f / 24.f, 1.f / 6.f), 0.5f));
+    const int dq = __float2int_rn(__fmul_rn(y, -274877906944.f)) + __float2int_rn(__fmul_rn(__fsub_rn(s, ye), 274877906944.f));  // in units of 2^-38
+    const u64 t = ct->powers[j & 63];
+    const u64 w = t + static_cast<u64>((static_cast<long long>(static_cast<int>(t >> 31)) * dq) >> 7);
+    return ((w >> (j >> 6)) + (1ull << (60 - kOne))) >> (61 - kOne);
+}
+
+// The bin of p (0 .. kBins - 1: p is at most the range that r.bins was made for), as the float that holds it.
+__device__ __forceinline__ float bin_float(const Row &r, float p) { return __fmaf_rn(p, r.bins, kMagic); }
+__device__ __forceinline__ int bin_of(const Row &r, float p) { return __float_as_int(bin_float(r, p)) - kMagicBits; }
 
 __device__ __forceinline__ u64 place(const Row &r, float p, float l, int idx)
 {
-    const int bin = min(kBins - 1, static_cast<int>(p * r.bins));
-    return static_cast<u64>(bin) << kBinShift | static_cast<u64>(order_of(l)) << kIdxBits | static_cast<u64>(idx);
+    return static_cast<u64>(bin_of(r, p)) << kBinShift | static_cast<u64>(order_of(l)) << kIdxBits | static_cast<u64>(idx);
 }
 
 // floor(f * z), and whether that is all of it; f in [0, 1).
@@ -198,213 +255,398 @@ __device__ __forceinline__ u64 part_of(float f, u64 z, bool &exact)
 }
 
 // ---- the block
-__device__ __forceinline__ u64 warp_min(u64 v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
 // The smallest a and the largest b of the block (all threads get them).
+template <int NT>
 __device__ __forceinline__ void block_range(Control *ct, u64 &a, u64 &b)
 {
-    const int w = threadIdx.x >> 5;
-    a = warp_min(a);
-    b = ~warp_min(~b);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    auto over = [&](int lanes) {
+        for (int o = lanes / 2; o > 0; o >>= 1) {
+            a = min(a, __shfl_xor_sync(0xffffffffu, a, o));
+            b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+    };
+    over(32);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
+    if (lane == 0) {
         ct->red[2 * w] = a;
         ct->red[2 * w + 1] = b;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        a = min(a, ct->red[2 * i]);
-        b = max(b, ct->red[2 * i + 1]);
-    }
+    a = ct->red[2 * (lane % (NT / 32))];
+    b = ct->red[2 * (lane % (NT / 32)) + 1];
+    over(NT / 32);
 }
 // Sums over the threads before this one; the block's sums in total.
+template <int NT>
 __device__ __forceinline__ void block_scan(Control *ct, u64 w, uint32_t n, u64 &before_w, uint32_t &before_n, u64 &all_w,
                                            uint32_t &all_n)
 {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    auto scan = [&](u64 &sw, uint32_t &sn) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 a = __shfl_up_sync(0xffffffffu, sw, o);
+            const uint32_t c = __shfl_up_sync(0xffffffffu, sn, o);
+            if (lane >= o) sw += a, sn += c;
+        }
+    };
     u64 sw = w;
     uint32_t sn = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 a = __shfl_up_sync(0xffffffffu, sw, o);
-        const uint32_t c = __shfl_up_sync(0xffffffffu, sn, o);
-        if (lane >= o) sw += a, sn += c;
-    }
+    scan(sw, sn);
     __syncthreads();
     if (lane == 31) {
         ct->scan_w[wid] = sw;
         ct->scan_n[wid] = sn;
     }
     __syncthreads();
-    before_w = sw - w, before_n = sn - n;
-    all_w = 0, all_n = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        if (i == wid) before_w += all_w, before_n += all_n;
-        all_w += ct->scan_w[i];
-        all_n += ct->scan_n[i];
-    }
+    u64 tw = lane < NT / 32 ? ct->scan_w[lane] : 0;
+    uint32_t tn = lane < NT / 32 ? ct->scan_n[lane] : 0;
+    scan(tw, tn);
+    all_w = __shfl_sync(0xffffffffu, tw, 31);
+    all_n = __shfl_sync(0xffffffffu, tn, 31);
+    const u64 ow = __shfl_sync(0xffffffffu, tw, (wid + 31) & 31);
+    const uint32_t on = __shfl_sync(0xffffffffu, tn, (wid + 31) & 31);
+    before_w = sw - w + (wid ? ow : 0);
+    before_n = sn - n + (wid ? on : 0);
 }
 
 // A part of a row, and the bins and the list beside it.
 template <typename IN>
 struct Part {
-    const IN *l;  // the part's logits, in shared memory
-    int n, first; // how many; the first one's index in the row
+    const IN *l;              // the part's logits
+    int n, first;             // how many; the first one's index in the row
     uint32_t *lo, *hi, *cnt;  // [kBins] weights in two words, tokens
-    u64 *list, *list_w;       // [kList] places; weights (of the first block)
-    __device__ __forceinline__ float logit(int i) const;
+    u64 *list, *list_w;       // [kList] places; weights
 };
-template <>
-__device__ __forceinline__ float Part<float>::logit(int i) const { return clean(l[i]); }
-template <>
-__device__ __forceinline__ float Part<uint16_t>::logit(int i) const { return clean(__uint_as_float(static_cast<uint32_t>(l[i]) << 16)); }
 
-__device__ __forceinline__ void add_weight(uint32_t *lo, uint32_t *hi, uint32_t *cnt, int bin, u64 w)
+// A part's logits by groups of 16 bytes, as they lie in memory; what is outside the part
+// counts as NaN.
+template <typename IN>
+struct Groups {
+    static constexpr int VEC = 16 / sizeof(IN);
+    const IN *l;
+    int n, from, count;  // from: the first group's first logit (negative: it begins before the part)
+    __device__ __forceinline__ explicit Groups(const Part<IN> &pt) : l(pt.l), n(pt.n)
+    {
+        const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(pt.l) & 15)) & 15) / static_cast<int>(sizeof(IN));
+        from = head == 0 ? 0 : head - VEC;
+        count = (n - from + VEC - 1) / VEC;
+    }
+    __device__ __forceinline__ uint4 load(int g) const
+    {
+        const uint32_t none = sizeof(IN) == 4 ? 0x7FC00000u : 0x7FC07FC0u;
+        const int at = from + g * VEC;
+        uint4 x = make_uint4(none, none, none, none);
+        if (at >= 0 && at + VEC <= n) {
+            x = *reinterpret_cast<const uint4 *>(l + at);
+        } else if (g < count) {
+            x = edge(at);
+        }
+        return x;
+    }
+    // A group that is partly outside.
+    __device__ __noinline__ uint4 edge(int at) const
+    {
+        const uint32_t none = sizeof(IN) == 4 ? 0x7FC00000u : 0x7FC07FC0u;
+        uint32_t w[4] = {none, none, none, none};
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (at + i >= 0 && at + i < n) {
+                if (sizeof(IN) == 4)
+                    w[i & 3] = reinterpret_cast<const uint32_t *>(l)[at + i];
+                else
+                    w[i / 2] = __byte_perm(w[i / 2], reinterpret_cast<const uint16_t *>(l)[at + i], i & 1 ? 0x5410 : 0x3254);
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // Logits h .. h + 3 of a group.
+    __device__ __forceinline__ static void four(const uint4 &x, int h, float (&v)[4])
+    {
+        if (sizeof(IN) == 4) {
+            v[0] = __uint_as_float(x.x), v[1] = __uint_as_float(x.y), v[2] = __uint_as_float(x.z), v[3] = __uint_as_float(x.w);
+        } else {
+            const uint32_t a = h ? x.z : x.x, b = h ? x.w : x.y;
+            v[0] = bf16_lo(a), v[1] = bf16_hi(a), v[2] = bf16_lo(b), v[3] = bf16_hi(b);
+        }
+    }
+};
+
+// f(four logits, their number in the turn) for all of the part, little work each: eight groups a
+// thread at a time (g, g + NT, ...), their loads in flight together; end(groups, g) after each turn.
+template <int NT, typename IN, typename F, typename E>
+__device__ __forceinline__ void each_light(const Part<IN> &pt, F f, E end)
+{
+    const Groups<IN> gr(pt);
+#pragma unroll 1
+    for (int g = threadIdx.x; (g & ~31) < gr.count; g += 8 * NT) {
+        uint4 x[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) x[y] = gr.load(g + y * NT);
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+#pragma unroll
+            for (int h = 0; h < gr.VEC; h += 4) {
+                float v[4];
+                gr.four(x[y], h, v);
+                f(v, y * (gr.VEC / 4) + h / 4);
+            }
+        end(gr, g);
+    }
+}
+
+// f(four logits) for all of the part, much work each: loads are four ahead, and the code of f is
+// there once (copies side by side ran out of the instruction cache).  Warps stay together.
+template <int NT, typename IN, typename F>
+__device__ __forceinline__ void each_four(const Part<IN> &pt, F f)
+{
+    const Groups<IN> gr(pt);
+    int g = threadIdx.x;
+    uint4 x[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) x[y] = gr.load(g + y * NT);
+#pragma unroll 1
+    for (; (g & ~31) < gr.count; g += NT) {
+        const uint4 next = gr.load(g + 4 * NT);
+#pragma unroll 1
+        for (int h = 0; h < gr.VEC; h += 4) {
+            float v[4];
+            gr.four(x[0], h, v);
+            f(v);
+        }
+        x[0] = x[1], x[1] = x[2], x[2] = x[3], x[3] = next;
+    }
+}
+
+__device__ __forceinline__ float select4(const float (&v)[4], int i) { return i & 2 ? (i & 1 ? v[3] : v[2]) : (i & 1 ? v[1] : v[0]); }
+
+__device__ __forceinline__ void add_weight(uint32_t *lo, uint32_t *hi, int bin, u64 w)
 {
     const uint32_t a = static_cast<uint32_t>(w), old = atomicAdd(lo + bin, a);
     const uint32_t b = static_cast<uint32_t>(w >> 32) + (old + a < old ? 1u : 0u);
     if (b) atomicAdd(hi + bin, b);
-    atomicAdd(cnt + bin, 1u);
 }
 
-// f(place, p, e) for each token of the part that is not masked and whose place is in [klo, khi].
-template <typename IN, typename F>
-__device__ __forceinline__ void each(const Part<IN> &pt, const Row &r, u64 klo, u64 khi, F f)
+template <int NT, typename IN>
+__device__ __forceinline__ void clear_bins(const Part<IN> &pt)
 {
-    for (int i = threadIdx.x; i < pt.n; i += kThreads) {
-        const float l = counted(r, pt.logit(i));
-        if (l == -INFINITY) continue;
-        float p, e;
-        exponent(r, l, p, e);
-        if (!(p < kNone)) continue;
-        const u64 k = place(r, p, l, pt.first + i);
-        if (k >= klo && k <= khi) f(k, p, e);
-    }
+    for (int i = threadIdx.x; i < kBins; i += NT) pt.lo[i] = pt.hi[i] = pt.cnt[i] = 0u;
+    __syncthreads();
 }
 
-// Tokens of places in [klo, khi] into bins of 2^shift places from klo on; the cluster's
-// sums end in the first block's bins.
-template <typename IN>
-__device__ __forceinline__ void histogram(const Part<IN> &pt, const Row &r, Control *ct, u64 klo, u64 khi, int shift, int rank,
-                                          int blocks)
+// The bins of all blocks added up in the first block's (each block's are complete).
+template <int NT, typename IN>
+__device__ __forceinline__ void reduce_bins(const Part<IN> &pt, int rank, int blocks)
 {
     const int tid = threadIdx.x;
-    for (int i = tid; i < kBins; i += kThreads) pt.lo[i] = pt.hi[i] = pt.cnt[i] = 0u;
-    __syncthreads();
-    each(pt, r, klo, khi, [&](u64 k, float p, float e) {
-        const u64 w = weight(ct->powers, p, e);
-        if (w != 0 && w >= r.least) add_weight(pt.lo, pt.hi, pt.cnt, static_cast<int>((k - klo) >> shift), w);
-    });
+    if (blocks == 1) {
+        __syncthreads();
+        return;
+    }
     cluster_sync();
-    if (blocks == 1) return;
     // each block adds up a share of the bins, in its own place for them (which no other reads)
     const int share = kBins / blocks;
-    for (int i = rank * share + tid; i < (rank + 1) * share; i += kThreads) {
-        u64 w = 0;
-        uint32_t n = 0;
-        for (int x = 0; x < blocks; ++x) {
-            w += static_cast<u64>(remote32(pt.hi + i, x)) << 32;
-            w += remote32(pt.lo + i, x);
-            n += remote32(pt.cnt + i, x);
+    for (int i = rank * share + tid; i < (rank + 1) * share; i += NT) {
+        uint32_t h[kMaxCluster], l[kMaxCluster], n[kMaxCluster];
+#pragma unroll
+        for (int x = 0; x < kMaxCluster; ++x) {
+            const int y = min(x, blocks - 1);
+            h[x] = remote32(pt.hi + i, y);
+            l[x] = remote32(pt.lo + i, y);
+            n[x] = remote32(pt.cnt + i, y);
         }
+        u64 w = 0;
+        uint32_t m = 0;
+#pragma unroll
+        for (int x = 0; x < kMaxCluster; ++x)
+            if (x < blocks) w += static_cast<u64>(h[x]) << 32 | l[x], m += n[x];
         pt.lo[i] = static_cast<uint32_t>(w);
         pt.hi[i] = static_cast<uint32_t>(w >> 32);
-        pt.cnt[i] = n;
+        pt.cnt[i] = m;
     }
     cluster_sync();
     if (rank != 0) return;
-    for (int i = share + tid; i < kBins; i += kThreads) {
-        const int x = i / share;
-        pt.lo[i] = remote32(pt.lo + i, x);
-        pt.hi[i] = remote32(pt.hi + i, x);
-        pt.cnt[i] = remote32(pt.cnt + i, x);
+    constexpr int IT = kBins / NT;
+    uint32_t h[IT], l[IT], n[IT];
+#pragma unroll
+    for (int y = 0; y < IT; ++y) {
+        const int i = tid + y * NT, x = i / share;
+        h[y] = remote32(pt.hi + i, x);
+        l[y] = remote32(pt.lo + i, x);
+        n[y] = remote32(pt.cnt + i, x);
+    }
+#pragma unroll
+    for (int y = 0; y < IT; ++y) {
+        const int i = tid + y * NT;
+        pt.hi[i] = h[y], pt.lo[i] = l[y], pt.cnt[i] = n[y];
     }
     __syncthreads();
 }
 
-// What the cluster does for the first block's question (all of its threads, after it was put).
-template <typename IN>
-__device__ __forceinline__ void answer(const Part<IN> &pt, const Row &r, Control *ct, int op, u64 klo, u64 khi, int shift, int rank,
-                                       int blocks)
+// The smallest a and the largest b of the cluster (all threads get them).
+template <int NT>
+__device__ __forceinline__ void gather_range(Control *ct, u64 &a, u64 &b, int rank, int blocks)
 {
     const int tid = threadIdx.x;
-    if (op == kRange) {
-        u64 a = ~0ull, b = 0ull;
-        each(pt, r, klo, khi, [&](u64 k, float p, float e) {
-            const u64 w = weight(ct->powers, p, e);
-            if (w != 0 && w >= r.least) a = min(a, k), b = max(b, k);
-        });
-        block_range(ct, a, b);
-        if (tid == 0) ct->mn = a, ct->mx = b;
-        cluster_sync();
-        if (rank == 0) {
-            for (int x = 1; x < blocks; ++x) a = min(a, remote64(&ct->mn, x)), b = max(b, remote64(&ct->mx, x));
-            __syncthreads();
-            if (tid == 0) ct->mn = a, ct->mx = b;
-            __syncthreads();
-        }
-    } else if (op == kHist) {
-        histogram(pt, r, ct, klo, khi, shift, rank, blocks);
-    } else {
-        if (tid == 0) ct->n = 0;
-        __syncthreads();
-        each(pt, r, klo, khi, [&](u64 k, float p, float e) {
-            const u64 w = weight(ct->powers, p, e);
-            if (w != 0 && w >= r.least) {
-                const int at = atomicAdd(&ct->n, 1);
-                if (at < kList) pt.list[at] = k;
-            }
-        });
-        cluster_sync();
-        if (rank == 0) {
-            int n = min(ct->n, kList);
-            for (int x = 1; x < blocks; ++x) {
-                const int m = min(static_cast<int>(remote32(&ct->n, x)), kList - n);
-                for (int i = tid; i < m; i += kThreads) pt.list[n + i] = remote64(pt.list + i, x);
-                n += m;
-            }
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads) {
-                float p, e;
-                exponent(r, logit_of(static_cast<uint32_t>(pt.list[i] >> kIdxBits)), p, e);
-                pt.list_w[i] = weight(ct->powers, p, e);
-            }
-            if (tid == 0) ct->n = n;
-            __syncthreads();
-        }
+    block_range<NT>(ct, a, b);
+    if (blocks == 1) return;
+    if (tid < blocks) {
+        put64(&ct->best[rank], tid, a);
+        put64(&ct->last[rank], tid, b);
     }
+    cluster_sync();
+    for (int x = 0; x < blocks; ++x) a = min(a, ct->best[x]), b = max(b, ct->last[x]);
+}
+
+// What the cluster does for the first block's question.
+template <int NT, typename IN>
+__device__ __forceinline__ void answer(const Part<IN> &pt, const Row &r, Control *ct, int rank, int blocks)
+{
+    const int tid = threadIdx.x, op = ct->op, shift = ct->shift;
+    const u64 klo = ct->klo, khi = ct->khi;
+    if (op == kHist) clear_bins<NT>(pt);
+    if (tid == 0) ct->n = 0;
+    __syncthreads();
+    // whole bins: what a token weighs is left for when they are side by side
+    const u64 inside = (1ull << kBinShift) - 1;
+    const bool whole = op == kGather && (klo & inside) == 0 && (khi & inside) == inside;
+    const int lo = static_cast<int>(klo >> kBinShift), hi = static_cast<int>(khi >> kBinShift);
+    const float blo = static_cast<float>(lo) + kMagic, bhi = static_cast<float>(hi) + kMagic;
+    // most tokens are told from their logits alone: outside the bins' bounds, a bin and some roundings wider
+    float most = r.max - (lo - 1) / r.bins / r.ch, least = r.max - (hi + 1) / r.bins / r.ch;
+    most += (fabsf(r.max) + fabsf(most)) * 0x1p-20f;
+    least -= (fabsf(r.max) + fabsf(least)) * 0x1p-20f;
+    if (!(r.bins > 0.f && r.ch > 0.f)) most = INFINITY, least = -INFINITY;
+    least = fmaxf(least, -3.402823466e38f);
+    if (r.infinite) least = INFINITY, most = INFINITY;
+    u64 a = ~0ull, b = 0ull;
+    u64 hits = 0;
+    each_light<NT>(
+        pt,
+        [&](const float(&v)[4], int q) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (v[i] >= least && v[i] <= most) m |= 1u << i;
+            hits |= static_cast<u64>(m) << (4 * q);
+        },
+        [&](const Groups<IN> &gr, int g) {
+#pragma unroll 1
+            for (; hits; hits &= hits - 1) {
+                const int x = __ffsll(static_cast<long long>(hits)) - 1, at = gr.from + (g + x / gr.VEC * NT) * gr.VEC + x % gr.VEC;
+                const int idx = pt.first + at;
+                float l = sizeof(IN) == 4 ? __uint_as_float(reinterpret_cast<const uint32_t *>(pt.l)[at])
+                                          : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(pt.l)[at]) << 16);
+                float p, e;
+                if (r.infinite) l = as_infinite(l);
+                exponent(r, l, p, e);
+                const float bin = bin_float(r, p);
+                if (!(p < kNone && bin >= blo && bin <= bhi)) continue;
+                if (!whole) {
+                    const u64 k = place(r, p, l, idx), w = weight(ct, p, e);
+                    if (k < klo || k > khi || w == 0 || w < r.least) continue;
+                    if (op == kRange) {
+                        a = min(a, k), b = max(b, k);
+                        continue;
+                    }
+                    if (op == kHist) {
+                        const int y = static_cast<int>((k - klo) >> shift);
+                        add_weight(pt.lo, pt.hi, y, w);
+                        atomicAdd(pt.cnt + y, 1u);
+                        continue;
+                    }
+                }
+                const int to = atomicAdd(&ct->n, 1);
+                if (to < kList) pt.list[to] = static_cast<u64>(__float_as_uint(l)) << 32 | static_cast<u64>(idx);
+            }
+            __syncwarp();
+        });
+    if (op == kRange) {
+        gather_range<NT>(ct, a, b, rank, blocks);
+        __syncthreads();  // (all have read the question)
+        if (tid == 0) ct->klo = a, ct->khi = b;
+        __syncthreads();
+        return;
+    }
+    if (op == kHist) {
+        reduce_bins<NT>(pt, rank, blocks);
+        return;
+    }
+    __syncthreads();
+    for (int i = tid, n = min(ct->n, kList); i < n; i += NT) {
+        const u64 v = pt.list[i];
+        const float l = __uint_as_float(static_cast<uint32_t>(v >> 32));
+        float p, e;
+        exponent(r, l, p, e);
+        const u64 w = weight(ct, p, e);
+        const bool in = w != 0 && w >= r.least;  // (a place behind all others if not)
+        pt.list[i] = in ? place(r, p, l, static_cast<int>(v & 0xFFFFFFFFu)) : ~0ull;
+        pt.list_w[i] = in ? w : 0ull;
+    }
+    if (blocks == 1) {
+        __syncthreads();
+        if (tid == 0) ct->all = ct->n, ct->n = min(ct->n, kList);
+        __syncthreads();
+        return;
+    }
+    if (tid == 0) put32(&ct->ns[rank], 0, ct->n);
+    cluster_sync();
+    if (rank != 0) return;
+    // the others' tokens behind its own: the i-th is the block's whose tokens cover i
+    int upto[kMaxCluster], all = 0;
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+        if (x < blocks) all += ct->ns[x];
+        upto[x] = all;
+    }
+    const int n = min(all, kList);
+    for (int i = min(upto[0], kList) + tid; i < n; i += NT) {
+        int x = 0, before = 0;
+#pragma unroll
+        for (int y = 0; y < kMaxCluster - 1; ++y)
+            if (i >= upto[y]) x = y + 1, before = upto[y];
+        const u64 k = remote64(pt.list + (i - before), x), w = remote64(pt.list_w + (i - before), x);
+        pt.list[i] = k;
+        pt.list_w[i] = w;
+    }
+    __syncthreads();
+    if (tid == 0) ct->n = n, ct->all = all;
+    __syncthreads();
 }
 
 // ---- the first block's decisions
-struct Found {
-    u64 key, w, upto;  // the token's place and weight, the weights up to it (it included)
-};
-
-template <typename IN>
+template <int NT, typename IN>
 struct Chooser {
+    static constexpr int kPer = kBins / NT;
     const Part<IN> &pt;
-    const Row &r;
     Control *ct;
     int blocks;
-    u64 w[kPer], before_w, all_w;  // the thread's bins of the first pass
+    bool counts;                   // the bins of the first pass have their tokens counted
+    int top_k;
+    float top_p, u;
+    u64 w[kPer], before_w, z;      // the thread's bins of the first pass; the weights that are left
     uint32_t n[kPer], before_n, all_n;
     u64 glo = 1, ghi = 0;          // places that the list covers (none)
+    // the target that is looked for: the first place at which the count (or the weights) reaches t, known to
+    // be in [klo, khi], with the sums before klo
+    int stage = 0, phase = 0, rounds = 0;
+    u64 t, klo, khi, bw;
+    uint32_t bn;
+    bool count;
+    u64 key, key_w;                // what was found last
 
-    __device__ __forceinline__ void ask(int op, u64 klo, u64 khi, int shift)
+    __device__ __forceinline__ void ask(int op, int shift)
     {
-        if (threadIdx.x == 0) ct->op = op, ct->klo = klo, ct->khi = khi, ct->shift = shift;
-        cluster_sync();
-        answer(pt, r, ct, op, klo, khi, shift, 0, blocks);
+        if (threadIdx.x < blocks) {  // to every block, so that none has to read it here
+            put32(&ct->op, threadIdx.x, op);
+            put32(&ct->shift, threadIdx.x, shift);
+            put64(&ct->klo, threadIdx.x, op == kGather ? glo : klo);
+            put64(&ct->khi, threadIdx.x, op == kGather ? ghi : khi);
+        }
     }
 
-    // Bins of the last pass, four a thread.
-    __device__ __forceinline__ void load_bins(u64 (&bw)[kPer], uint32_t (&bn)[kPer], u64 &bef_w, uint32_t &bef_n, u64 &tot_w,
+    // Bins of the last pass, a few a thread.
+    __device__ __forceinline__ void load_bins(u64 (&xw)[kPer], uint32_t (&xn)[kPer], u64 &bef_w, uint32_t &bef_n, u64 &tot_w,
                                               uint32_t &tot_n)
     {
         u64 sw = 0;
@@ -412,104 +654,163 @@ struct Chooser {
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
             const int i = kPer * threadIdx.x + q;
-            bw[q] = static_cast<u64>(pt.hi[i]) << 32 | pt.lo[i];
-            bn[q] = pt.cnt[i];
-            sw += bw[q];
-            sn += bn[q];
+            xw[q] = static_cast<u64>(pt.hi[i]) << 32 | pt.lo[i];
+            xn[q] = pt.cnt[i];
+            sw += xw[q];
+            sn += xn[q];
         }
-        block_scan(ct, sw, sn, bef_w, bef_n, tot_w, tot_n);
+        block_scan<NT>(ct, sw, sn, bef_w, bef_n, tot_w, tot_n);
     }
 
     // The bin at which the sums before it (base) and in order reach t.
     template <int Q>
-    __device__ __forceinline__ void find_bin(const u64 (&bw)[Q], const uint32_t (&bn)[Q], u64 bef_w, uint32_t bef_n, u64 base_w,
-                                             uint32_t base_n, u64 t, bool count)
+    __device__ __forceinline__ void find_bin(const u64 (&xw)[Q], const uint32_t (&xn)[Q], u64 bef_w, uint32_t bef_n, u64 base_w,
+                                             uint32_t base_n)
     {
         u64 cw = base_w + bef_w;
         uint32_t cn = base_n + bef_n;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const u64 a = count ? cn : cw, b = count ? cn + bn[q] : cw + bw[q];
+            const u64 a = count ? cn : cw, b = count ? cn + xn[q] : cw + xw[q];
             if (a < t && t <= b) {
                 ct->bin = Q * threadIdx.x + q;
                 ct->base_w = cw;
                 ct->base_n = cn;
-                ct->bin_n = bn[q];
+                ct->bin_n = xn[q];
             }
-            cw += bw[q];
-            cn += bn[q];
+            cw += xw[q];
+            cn += xn[q];
         }
         __syncthreads();
     }
 
-    // The first token at which the count (or the weights) reaches t, 1 <= t <= all of them.
-    __device__ Found find(u64 t, bool count)
+    // The next target; whether there is one.
+    __device__ __forceinline__ bool next_target()
     {
-        find_bin(w, n, before_w, before_n, 0, 0, t, count);
-        u64 klo = static_cast<u64>(ct->bin) << kBinShift, khi = klo + ((1ull << kBinShift) - 1), bw = ct->base_w;
-        uint32_t bn = ct->base_n, m = ct->bin_n;
-        __syncthreads();
-        if (klo < glo || khi > ghi) {
-            if (bn + m <= kList) {
-                glo = 0;
-            } else {
-                // many tokens in a bin: parts of its range, until few are left (each round leaves
-                // 11 bits less of a place's 64)
-                for (int round = 0; m > kList && round < 6; ++round) {
-                    ask(kRange, klo, khi, 0);
-                    klo = ct->mn;
-                    const u64 span = ct->mx - klo;
-                    const int shift = max(0, 64 - __clzll(span) - 11);
-                    ask(kHist, klo, ct->mx, shift);
-                    u64 xw[kPer], xbw, xall;
-                    uint32_t xn[kPer], xbn, xalln;
-                    load_bins(xw, xn, xbw, xbn, xall, xalln);
-                    find_bin(xw, xn, xbw, xbn, bw, bn, t, count);
-                    klo += static_cast<u64>(ct->bin) << shift;
-                    khi = klo + ((1ull << shift) - 1);
-                    bw = ct->base_w, bn = ct->base_n, m = ct->bin_n;
-                    __syncthreads();
-                }
-                glo = klo;
+        bool exact = true;
+        if (stage == 0) {
+            ++stage;
+            if (top_k > 0 && static_cast<uint32_t>(top_k) < all_n) {
+                t = top_k, count = true;
+                return true;
             }
-            ghi = khi;
-            ask(kGather, glo, ghi, 0);
         }
-        return look(klo, khi, bw, bn, t, count);
+        count = false;
+        if (stage == 1) {
+            ++stage;
+            if (top_p < 1.f) {
+                t = top_p > 0.f ? part_of(top_p, z, exact) : 0ull;
+                t = max(1ull, t + (exact ? 0 : 1));
+                return true;
+            }
+        }
+        t = u >= 1.f ? z : (u > 0.f ? min(z, part_of(u, z, exact) + 1) : 1ull);
+        return ++stage == 3;
     }
 
-    // The same among the listed tokens in [klo, khi], with the sums before klo.
-    __device__ Found look(u64 klo, u64 khi, u64 bw, uint32_t bn, u64 t, bool count)
+    // Goes on until something has to be asked of the cluster (true) or the token is found.
+    __device__ __forceinline__ bool go_on()
+    {
+        for (;;) {
+            if (phase == 0) {  // a new target
+                if (!next_target()) return false;
+                find_bin(w, n, before_w, before_n, 0, 0);
+                klo = static_cast<u64>(ct->bin) << kBinShift, khi = klo + ((1ull << kBinShift) - 1);
+                bw = ct->base_w, bn = ct->base_n;
+                const uint32_t m = ct->bin_n;
+                __syncthreads();
+                phase = 4;
+                if (klo < glo || khi > ghi) {
+                    if (counts && m > kList) {
+                        ask(kRange, 0);
+                        phase = 2;
+                    } else {
+                        // all tokens up to the bin's, where they are few (what is asked next lies among them)
+                        glo = counts && bn + m <= kList ? 0 : klo, ghi = khi;
+                        ask(kGather, 0);
+                        phase = 1;
+                    }
+                    return true;
+                }
+            } else if (phase == 1) {  // after a list
+                phase = 4;
+                if (ct->all > kList && rounds < 6) {
+                    ask(kRange, 0);
+                    phase = 2;
+                    return true;
+                }
+            } else if (phase == 2) {
+                // many tokens in a bin: parts of its range, until few are left (each round
+                // leaves kBinBits less of a place's bits)
+                klo = ct->klo, khi = ct->khi;
+                __syncthreads();
+                ask(kHist, max(0, 64 - __clzll(khi - klo) - kBinBits));  // (khi - klo) >> shift < kBins
+                phase = 3;
+                return true;
+            } else if (phase == 3) {
+                const int shift = ct->shift;
+                u64 xw[kPer], xbw, xall;
+                uint32_t xn[kPer], xbn, xalln;
+                load_bins(xw, xn, xbw, xbn, xall, xalln);
+                find_bin(xw, xn, xbw, xbn, bw, bn);
+                klo += static_cast<u64>(ct->bin) << shift;
+                khi = klo + ((1ull << shift) - 1);
+                bw = ct->base_w, bn = ct->base_n;
+                const uint32_t m = ct->bin_n;
+                __syncthreads();
+                if (m > kList && ++rounds < 6) {
+                    ask(kRange, 0);
+                    phase = 2;
+                } else {
+                    glo = klo, ghi = khi;
+                    ask(kGather, 0);
+                    phase = 1;
+                }
+                return true;
+            } else {
+                look();
+                phase = rounds = 0;
+            }
+        }
+    }
+
+    // The target's place among the listed tokens in [klo, khi].
+    __device__ __forceinline__ void look()
     {
         const int tid = threadIdx.x, lane = tid & 31, len = ct->n;
+#pragma unroll 1
         for (int round = 0;; ++round) {  // (each leaves 9 bits less)
             u64 a = ~0ull, b = 0ull;
             if (tid == 0) ct->few = 0;
             __syncthreads();
-            for (int i = tid; i < len; i += kThreads) {
+            for (int i = tid; i < len; i += NT) {
                 const u64 k = pt.list[i];
                 if (k < klo || k > khi) continue;
                 a = min(a, k), b = max(b, k);
                 const int at = atomicAdd(&ct->few, 1);
                 if (at < kFew) ct->small[at] = i;
             }
-            block_range(ct, a, b);
+            __syncthreads();
             if (ct->few <= kFew || round == 8) break;
+            block_range<NT>(ct, a, b);
             klo = a;
-            const int shift = max(0, 64 - __clzll(b - a) - 9);  // (b - a) >> shift < kThreads
+            const int shift = max(0, 64 - __clzll(b - a) - (NT == 1024 ? 10 : 9));  // (b - a) >> shift < NT
             pt.lo[tid] = pt.hi[tid] = pt.cnt[tid] = 0u;
             __syncthreads();
-            for (int i = tid; i < len; i += kThreads) {
+            for (int i = tid; i < len; i += NT) {
                 const u64 k = pt.list[i];
-                if (k >= klo && k <= khi) add_weight(pt.lo, pt.hi, pt.cnt, static_cast<int>((k - klo) >> shift), pt.list_w[i]);
+                if (k < klo || k > khi) continue;
+                const int y = static_cast<int>((k - klo) >> shift);
+                add_weight(pt.lo, pt.hi, y, pt.list_w[i]);
+                atomicAdd(pt.cnt + y, 1u);
             }
             __syncthreads();
             const u64 xw[1] = {static_cast<u64>(pt.hi[tid]) << 32 | pt.lo[tid]};
             const uint32_t xn[1] = {pt.cnt[tid]};
             u64 xbw, xall;
             uint32_t xbn, xalln;
-            block_scan(ct, xw[0], xn[0], xbw, xbn, xall, xalln);
-            find_bin(xw, xn, xbw, xbn, bw, bn, t, count);
+            block_scan<NT>(ct, xw[0], xn[0], xbw, xbn, xall, xalln);
+            find_bin(xw, xn, xbw, xbn, bw, bn);
             klo += static_cast<u64>(ct->bin) << shift;
             khi = min(khi, klo + ((1ull << shift) - 1));
             bw = ct->base_w, bn = ct->base_n;
@@ -520,6 +821,7 @@ struct Chooser {
             const u64 k = lane < few ? pt.list[ct->small[lane]] : ~0ull, mine = lane < few ? pt.list_w[ct->small[lane]] : 0ull;
             u64 cw = bw;
             uint32_t cn = bn;
+#pragma unroll 1
             for (int i = 0; i < few; ++i) {
                 const u64 ok = __shfl_sync(0xffffffffu, k, i), ow = __shfl_sync(0xffffffffu, mine, i);
                 if (ok < k) cw += ow, ++cn;
@@ -528,133 +830,262 @@ struct Chooser {
             if (lane < few && c0 < t && t <= c1) ct->key_found = k, ct->w_found = mine, ct->base_w = cw + mine;
         }
         __syncthreads();
-        const Found f{ct->key_found, ct->w_found, ct->base_w};
+        key = ct->key_found, key_w = ct->w_found;
+        if (stage < 3) z = ct->base_w;  // (the weights up to it, its own included)
         __syncthreads();
-        return f;
     }
 };
 
 struct Params {
     moe_sample_desc d;
-    int part;  // logits of a block
+    int part;    // logits of a block
+    int blocks;  // of a row: a cluster
 };
 
 __device__ __forceinline__ float setting(const float *a, float one, int t) { return a ? a[t] : one; }
 
-template <typename IN>
-__global__ void __launch_bounds__(kThreads, 2) moe_sample_kernel(const __grid_constant__ Params p, int blocks)
+// NT threads; COUNT: 16-bit logits are counted by value first.
+template <typename IN, int NT, bool COUNT>
+__global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_constant__ Params p)
 {
+    const int blocks = p.blocks;
     extern __shared__ __align__(16) uint8_t smem[];
     Control *ct = reinterpret_cast<Control *>(smem);
     u64 *list = reinterpret_cast<u64 *>(smem + (sizeof(Control) + 15) / 16 * 16);
     uint32_t *bins = reinterpret_cast<uint32_t *>(list + 2 * kList);
-    IN *buf = reinterpret_cast<IN *>(bins + 3 * kBins);
+    uint32_t *counters = bins + 3 * kBins;  // COUNT: [kCounters / 2]
     const moe_sample_desc &d = p.d;
-    const int tid = threadIdx.x, rank = cluster_rank(), t = blockIdx.x / blocks;
+    const int tid = threadIdx.x, lane = tid & 31, rank = cluster_rank(), t = blockIdx.x / blocks;
     const int first = min(rank * p.part, d.V), n = min(p.part, d.V - first);
-    const Part<IN> pt{buf, n, first, bins, bins + kBins, bins + 2 * kBins, list, list + kList};
-    if (tid < 64) ct->powers[tid] = kPowers.v[tid];
+    const Part<IN> pt{static_cast<const IN *>(d.logits_dev) + static_cast<long long>(t) * d.stride + first, n, first,
+                      bins, bins + kBins, bins + 2 * kBins, list, list + kList};
+    if (tid < 64) {
+        const u64 v = kPowers.v[tid];
+        ct->powers[tid] = v;
+        ct->powers32[tid] = static_cast<int>((v + (1ull << 30)) >> 31);
+    }
+    if (COUNT)
+        for (int i = tid; i < kCounters / 8; i += NT) reinterpret_cast<uint4 *>(counters)[i] = make_uint4(0u, 0u, 0u, 0u);
+    clear_bins<NT>(pt);
+    if (blocks > 1) cluster_arrive();
     grid_wait();
     grid_release();
 
-    // ---- the part's logits; the first in order, the smallest that is not masked
-    const IN *src = static_cast<const IN *>(d.logits_dev) + static_cast<long long>(t) * d.stride + first;
-    u64 best = ~0ull;
-    float low = INFINITY;
-    for (int i0 = tid; i0 < n; i0 += 8 * kThreads) {
-        IN v[8];
+    // ---- the largest logit, the smallest that is not masked (as orders: the least, the greatest)
+    u64 best = ~0ull, last = 0ull;
+    bool counted = COUNT;  // 16-bit logits are counted by value
+    if (COUNT) {
+        uint32_t over = 0;  // tokens that were counted, and then are not found
+        each_light<NT>(
+            pt,
+            [&](const float(&v)[4], int) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-            if (i0 + x * kThreads < n) v[x] = src[i0 + x * kThreads];
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = __float_as_uint(v[i]) >> 16;
+                    if (!(v[i] > -INFINITY)) continue;  // masked (many at one place), NaN
+                    atomicAdd(counters + (x >> 1), 1u << (16 * (x & 1)));
+                    ++over;
+                }
+            },
+            [](const Groups<IN> &, int) {});
+        __syncthreads();
+#pragma unroll 1
+        for (int i = tid; i < kCounters / 8; i += NT) {
+            const uint4 c = reinterpret_cast<const uint4 *>(counters)[i];
+            if ((c.x | c.y | c.z | c.w) == 0) continue;
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-            if (i0 + x * kThreads < n) {
-                const int i = i0 + x * kThreads;
-                buf[i] = v[x];
-                const float l = pt.logit(i);
-                best = min(best, static_cast<u64>(order_of(l)) << kIdxBits | static_cast<u64>(first + i));
-                if (l > -INFINITY) low = fminf(low, l);
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t m = u4w(c, x >> 1) >> (16 * (x & 1)) & 0xFFFFu;
+                over -= m;
+                if (m != 0) {
+                    const u64 o = order_of(__uint_as_float(static_cast<uint32_t>(8 * i + x) << 16));
+                    best = min(best, o), last = max(last, o);
+                }
             }
+        }
+        u64 z0, z1;
+        uint32_t z2, all;
+        block_scan<NT>(ct, 0, over, z0, z2, z1, all);
+        counted = all == 0;  // (else a counter ran over its 16 bits: every token is looked at instead)
     }
-    u64 last = low == INFINITY ? 0ull : order_of(low);
-    block_range(ct, best, last);
-    if (tid == 0) ct->mn = best, ct->mx = last;
-    cluster_sync();
-    for (int x = 0; x < blocks; ++x) {
-        best = min(best, remote64(&ct->mn, x));
-        last = max(last, remote64(&ct->mx, x));
+    if (!counted) {
+        float top = -INFINITY, low = INFINITY;
+        each_light<NT>(
+            pt,
+            [&](const float(&v)[4], int) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    top = fmaxf(top, v[i]);  // (NaN is none)
+                    if (v[i] > -INFINITY) low = fminf(low, v[i]);
+                }
+            },
+            [](const Groups<IN> &, int) {});
+        best = order_of(top);
+        last = low == INFINITY ? 0ull : order_of(low);
     }
+    if (blocks > 1) cluster_wait();
+    gather_range<NT>(ct, best, last, rank, blocks);
     Row r;
-    r.max = logit_of(static_cast<uint32_t>(best >> kIdxBits));
-    const int top = static_cast<int>(best & (MOE_SAMPLE_MAX_VOCAB - 1));
+    r.max = best == ~0ull ? -INFINITY : logit_of(static_cast<uint32_t>(best));
     const float temperature = setting(d.temperature_dev, d.temperature, t);
     const int top_k = d.top_k_dev ? d.top_k_dev[t] : d.top_k;
     const bool nothing = r.max == -INFINITY;
     if (nothing || !(temperature > kGreedy) || top_k == 1) {
+        u64 at = ~0ull, none = 0ull;  // the first of the largest
+        u64 hits = 0;
+        if (!nothing)
+            each_light<NT>(
+                pt,
+                [&](const float(&v)[4], int q) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (v[i] == r.max) m |= 1u << i;
+                    hits |= static_cast<u64>(m) << (4 * q);
+                },
+                [&](const Groups<IN> &gr, int g) {
+                    if (hits) {
+                        const int x = __ffsll(static_cast<long long>(hits)) - 1;
+                        at = min(at, static_cast<u64>(first + gr.from + (g + x / gr.VEC * NT) * gr.VEC + x % gr.VEC));
+                    }
+                    hits = 0;
+                });
+        if (blocks > 1) cluster_sync();  // what the last exchange left has been read
+        gather_range<NT>(ct, at, none, rank, blocks);
         if (rank == 0 && tid == 0) {
-            d.token_dev[t] = nothing ? -1 : top;
+            d.token_dev[t] = nothing ? -1 : static_cast<int32_t>(at);
             if (d.prob_dev) d.prob_dev[t] = nothing ? 0.f : 1.f;
         }
-        cluster_sync();  // nobody's shared memory is read any more
         return;
     }
-    const double c = 1.4426950408889634074 / static_cast<double>(temperature);
-    r.ch = static_cast<float>(c);
-    r.cl = static_cast<float>(c - static_cast<double>(r.ch));
+    // log2(e) / t in two floats, from log2(e) in two
+    r.ch = 1.44269502f / temperature;
+    r.cl = temperature < INFINITY ? (fmaf(-r.ch, temperature, 1.44269502f) + 1.92596303e-8f) / temperature : 0.f;
     r.infinite = r.max == INFINITY;
     if (r.infinite) r.max = 0.f;
-    const float least = setting(d.min_p_dev, d.min_p, t);
-    r.least = least > 0.f ? static_cast<u64>(ceil(static_cast<double>(fminf(least, 1.f)) * 35184372088832.0)) : 1ull;
-    const float range = r.infinite ? 0.f : fminf((r.max - logit_of(static_cast<uint32_t>(last))) * r.ch, kNone);
-    r.bins = range > 0.f ? kBins / range : 0.f;
+    const float least = setting(d.min_p_dev, d.min_p, t), top_p = setting(d.top_p_dev, d.top_p, t);
+    bool exact = true;
+    r.least = least >= 1.f ? 1ull << kOne : (least > 0.f ? part_of(least, 1ull << kOne, exact) : 1ull);
+    if (!exact) ++r.least;
+    const float range = r.infinite ? 0.f : fminf(__fmul_rn(__fsub_rn(r.max, logit_of(static_cast<uint32_t>(last))), r.ch), kNone);
+    r.bins = range > 1e-30f ? (kBins - 1) / range : 0.f;  // (else all in one)
 
-    histogram(pt, r, ct, 0ull, ~0ull, kBinShift, rank, blocks);
-    if (rank != 0) {
-        for (;;) {
-            cluster_sync();  // a question
-            const int op = remote32(&ct->op, 0);
-            if (op == kDone) break;
-            answer(pt, r, ct, op, remote64(&ct->klo, 0), remote64(&ct->khi, 0), remote32(&ct->shift, 0), rank, blocks);
+    // ---- the first pass: every token that counts into its bin
+    const bool counts = top_k > 0 || top_p < 1.f;  // (else the one question needs none)
+    auto into_bin = [&](float x, float e, uint32_t count) {
+        const u64 w = weight(ct, x, e);
+        if (w == 0 || w < r.least) return;
+        const int bin = bin_of(r, x);
+        add_weight(pt.lo, pt.hi, bin, w * count);
+        if (counts) atomicAdd(pt.cnt + bin, count);
+    };
+    if (counted && !r.infinite) {
+#pragma unroll 1
+        for (int i = tid; i < kCounters / 8; i += NT) {
+            const uint4 c = reinterpret_cast<const uint4 *>(counters)[i];
+            if ((c.x | c.y | c.z | c.w) == 0) continue;
+#pragma unroll 1
+            for (int y = 0; y < 8; ++y) {
+                const uint32_t m = (y & 4 ? (y & 2 ? c.w : c.z) : (y & 2 ? c.y : c.x)) >> (16 * (y & 1)) & 0xFFFFu;
+                if (m == 0) continue;
+                float x, e;
+                exponent(r, __uint_as_float(static_cast<uint32_t>(8 * i + y) << 16), x, e);
+                into_bin(x, e, m);
+            }
         }
-        cluster_sync();
-        return;
+    } else {
+        // small weights side by side in 32 bits; the others wait in the warp's queue (in the
+        // list's place) until there are 32 of them
+        const uint32_t least32 = static_cast<uint32_t>(min(r.least, static_cast<u64>(0xFFFFFFFFu)));
+        float2 *queue = reinterpret_cast<float2 *>(pt.list) + (tid >> 5) * 64;
+        int waiting = 0;
+        each_four<NT>(pt, [&](const float(&v)[4]) {
+            float x[4], e[4];
+            uint32_t w[4], was[4], large = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                exponent(r, r.infinite ? as_infinite(v[i]) : v[i], x[i], e[i]);
+                if (x[i] < kSmall) large |= 1u << i;
+                w[i] = small_weight(ct, x[i], e[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                was[i] = 0u;
+                if (w[i] >= least32) was[i] = atomicAdd(pt.lo + bin_of(r, x[i]), w[i]);
+            }
+            if (counts) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (w[i] >= least32) atomicAdd(pt.cnt + bin_of(r, x[i]), 1u);
+            }
+            bool carry = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) carry |= was[i] > ~w[i];
+            if (carry) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (was[i] > ~w[i]) atomicAdd(pt.hi + bin_of(r, x[i]), 1u);
+            }
+#pragma unroll 1
+            for (;;) {
+                const uint32_t have = __ballot_sync(0xffffffffu, large != 0);
+                if (have == 0) break;
+                if (large != 0) {
+                    const int i = __ffs(large) - 1;
+                    large &= large - 1;
+                    queue[waiting + __popc(have & ((1u << lane) - 1u))] = make_float2(select4(x, i), select4(e, i));
+                }
+                waiting += __popc(have);
+                __syncwarp();
+                if (waiting >= 32) {
+                    waiting -= 32;
+                    const float2 q = queue[waiting + lane];
+                    into_bin(q.x, q.y, 1u);
+                    __syncwarp();
+                }
+            }
+        });
+        if (lane < waiting) into_bin(queue[lane].x, queue[lane].y, 1u);
     }
-    Chooser<IN> ch{pt, r, ct, blocks};
-    ch.load_bins(ch.w, ch.n, ch.before_w, ch.before_n, ch.all_w, ch.all_n);
-    u64 z = ch.all_w;
-    if (top_k > 0 && static_cast<uint32_t>(top_k) < ch.all_n) z = ch.find(top_k, true).upto;
-    const float top_p = setting(d.top_p_dev, d.top_p, t);
-    if (top_p < 1.f) {
-        bool exact = true;
-        const u64 f = top_p > 0.f ? part_of(top_p, z, exact) : 0ull;
-        z = ch.find(max(1ull, f + (exact ? 0 : 1)), false).upto;
+    reduce_bins<NT>(pt, rank, blocks);
+
+    // ---- questions, until the first block has found the token
+    Chooser<NT, IN> ch{pt, ct, blocks, counts, top_k, top_p, 0.f};
+    if (rank == 0) {
+        ch.u = d.u_dev[t];
+        ch.load_bins(ch.w, ch.n, ch.before_w, ch.before_n, ch.z, ch.all_n);
     }
-    const float u = d.u_dev[t];
-    bool exact;
-    const Found f = ch.find(u >= 1.f ? z : (u > 0.f ? min(z, part_of(u, z, exact) + 1) : 1ull), false);
-    if (tid == 0) {
-        d.token_dev[t] = static_cast<int32_t>(f.key & (MOE_SAMPLE_MAX_VOCAB - 1));
-        if (d.prob_dev) d.prob_dev[t] = static_cast<float>(static_cast<double>(f.w) / static_cast<double>(z));
+#pragma unroll 1
+    for (;;) {
+        if (rank == 0 && !ch.go_on()) {
+            if (tid == 0) {
+                d.token_dev[t] = static_cast<int32_t>(ch.key & (MOE_SAMPLE_MAX_VOCAB - 1));
+                if (d.prob_dev) d.prob_dev[t] = static_cast<float>(static_cast<double>(ch.key_w) / static_cast<double>(ch.z));
+            }
+            if (blocks == 1) return;
+            ch.ask(kDone, 0);
+        }
+        if (blocks > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        if (ct->op == kDone) return;  // (nobody's shared memory is read any more)
+        answer<NT>(pt, r, ct, rank, blocks);
     }
-    if (tid == 0) ct->op = kDone;
-    cluster_sync();
-    cluster_sync();
 }
 
-template <typename IN>
-cudaError_t launch_in(const moe_sample_desc &d, cudaStream_t st)
+template <typename IN, int NT, bool COUNT>
+cudaError_t launch_one(const Params &p, cudaStream_t st)
 {
-    int blocks = 1;
-    while (blocks < kMaxCluster && d.V > 4096 * blocks) blocks *= 2;
-    Params p{d, (d.V + blocks - 1) / blocks};
-    const int smem = static_cast<int>((sizeof(Control) + 15) / 16 * 16 + 2 * kList * 8 + 3 * kBins * 4) + (p.part * static_cast<int>(sizeof(IN)) + 15) / 16 * 16;
-    auto *fn = moe_sample_kernel<IN>;
+    const int blocks = p.blocks;
+    constexpr int smem = static_cast<int>((sizeof(Control) + 15) / 16 * 16 + 2 * kList * 8 + 3 * kBins * 4) + (COUNT ? kCounters * 2 : 0);
+    auto *fn = moe_sample_kernel<IN, NT, COUNT>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3(d.T * blocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(p.d.T * blocks);
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -664,14 +1095,25 @@ cudaError_t launch_in(const moe_sample_desc &d, cudaStream_t st)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fn, p, blocks);
+    return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 }  // namespace
 
-cudaError_t launch_sample(const moe_sample_desc &d, cudaStream_t st)
+cudaError_t launch_sample(const moe_sample_desc &d, int num_sms, cudaStream_t st)
 {
-    return d.bf16 ? launch_in<uint16_t>(d, st) : launch_in<float>(d, st);
+    // as many blocks a row as there is room for, each with 2048 logits or more
+    auto split = [&](int room) {
+        int blocks = 1;
+        while (blocks < kMaxCluster && d.V > 4096 * blocks && 2LL * d.T * blocks <= room) blocks *= 2;
+        return Params{d, (d.V + blocks - 1) / blocks, blocks};
+    };
+    // Counters leave room for one block an SM, and pay where it has much to count.  Measured, with them
+    // and without: parts of 65543, 67 / 152 us (152 rows) and 54 / 85 (64 rows of two parts); of 32769,
+    // 39 / 52 (24 rows of four); of 20000, 45 / 45 (64 rows of two); of 16385, 50 / 46 (16 rows of eight).
+    const Params c = split(num_sms), p = split(2 * num_sms);
+    if (!d.bf16) return launch_one<float, 512, false>(p, st);
+    return c.part >= 24576 ? launch_one<uint16_t, 1024, true>(c, st) : launch_one<uint16_t, 512, false>(p, st);
 }
 
 }  // namespace moe

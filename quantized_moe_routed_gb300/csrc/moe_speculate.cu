@@ -157,7 +157,7 @@ moe_status_t moe_sample(const moe_sample_desc *desc, void *stream)
     moe::Device dev;
     const moe_status_t st = moe::query_device(-1, &dev);
     if (st != MOE_OK) return st;
-    return launched(moe::launch_sample(d, static_cast<cudaStream_t>(stream)), "sampling launch");
+    return launched(moe::launch_sample(d, dev.sms, static_cast<cudaStream_t>(stream)), "sampling launch");
 }
 
 }  // extern "C"

@@ -8,6 +8,6 @@ namespace moe {
 
 MOE_FAKE_LAUNCH(launch_kv_compact, const CompactParams &, cudaStream_t)
 MOE_FAKE_LAUNCH(launch_kv_fork, const ForkParams &, cudaStream_t)
-MOE_FAKE_LAUNCH(launch_sample, const moe_sample_desc &, cudaStream_t)
+MOE_FAKE_LAUNCH(launch_sample, const moe_sample_desc &, int, cudaStream_t)
 
 }  // namespace moe

@@ -83,6 +83,33 @@ def test_flat_and_steep_rows(V, spread):
         _compare(y, _u(8, 6), k=V // 2, p=0.99)
 
 
+def test_many_rows_of_16_bits():
+    """Logits that are counted by value: whole rows of one value (more than a counter holds; twice 2^16), two
+    values, infinite and masked and NaN ones beside ordinary rows."""
+    T, V = 80, 131072
+    x = _logits(T, V, 21, half=True)
+    x[0] = 0.0
+    x[1] = -3.0
+    x[1, 70000:] = 2.0
+    x[2, ::2] = -math.inf
+    x[3] = -math.inf
+    x[4] = math.nan
+    x[5, 100], x[5, 99999] = math.inf, math.inf
+    x[6] = 1.0
+    x[6, ::2] = -1.0
+    x[7, :65536] = 5.0
+    x[8] = -0.0
+    x[8, 1::2] = 0.0
+    x[9] = -math.inf
+    x[9, 131071] = -7.0
+    u = _u(T, 22)
+    _compare(x, u)
+    _compare(x, u, t=0.8, k=70000, p=0.97)
+    _compare(x[:, 1:], u, t=[0.0, 1.0] * (T // 2), mp=0.05)
+    tok = sample(x[:1].repeat(T, 1).to(DEV), (torch.arange(T) / T).to(DEV))
+    assert tok.tolist() == [int(math.floor(float(torch.tensor(i / T)) * V)) for i in range(T)]
+
+
 def test_ties_go_to_the_lowest_index():
     """All logits equal, and two values: ranks are indices, exactly, at every u."""
     V, T = 10007, 64

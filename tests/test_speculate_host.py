@@ -47,7 +47,7 @@ def test_kernels_fit_their_registers(unit, regs):
     used = [int(r) for r in re.findall(r"Used (\d+) registers", text)]
     spills = [int(a) + int(b) for a, b in re.findall(r"(\d+) bytes spill stores, (\d+) bytes spill loads", text)]
     assert used and max(used) <= regs, used
-    assert max(spills) <= 256, spills
+    assert max(spills) <= 768, spills  # (around the passes: what the first block's decisions keep)
 
 
 def _sample(logits=A, stride=100, bf16=0, T=2, V=100, u=A, t=None, k=None, p=None, mp=None, token=A, prob=None):
