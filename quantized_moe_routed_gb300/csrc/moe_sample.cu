@@ -870,6 +870,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_
     if (blocks > 1) cluster_arrive();
     grid_wait();
     grid_release();
+    // (the settings are here by the time they are used)
+    const float temperature = setting(d.temperature_dev, d.temperature, t), top_p = setting(d.top_p_dev, d.top_p, t);
+    const float min_p = setting(d.min_p_dev, d.min_p, t), u = d.u_dev[t];
+    const int top_k = d.top_k_dev ? d.top_k_dev[t] : d.top_k;
 
     // ---- the largest logit, the smallest that is not masked (as orders: the least, the greatest)
     u64 best = ~0ull, last = 0ull;
@@ -927,8 +931,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_
     gather_range<NT>(ct, best, last, rank, blocks);
     Row r;
     r.max = best == ~0ull ? -INFINITY : logit_of(static_cast<uint32_t>(best));
-    const float temperature = setting(d.temperature_dev, d.temperature, t);
-    const int top_k = d.top_k_dev ? d.top_k_dev[t] : d.top_k;
     const bool nothing = r.max == -INFINITY;
     if (nothing || !(temperature > kGreedy) || top_k == 1) {
         u64 at = ~0ull, none = 0ull;  // the first of the largest
@@ -963,9 +965,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_
     r.cl = temperature < INFINITY ? (fmaf(-r.ch, temperature, 1.44269502f) + 1.92596303e-8f) / temperature : 0.f;
     r.infinite = r.max == INFINITY;
     if (r.infinite) r.max = 0.f;
-    const float least = setting(d.min_p_dev, d.min_p, t), top_p = setting(d.top_p_dev, d.top_p, t);
     bool exact = true;
-    r.least = least >= 1.f ? 1ull << kOne : (least > 0.f ? part_of(least, 1ull << kOne, exact) : 1ull);
+    r.least = min_p >= 1.f ? 1ull << kOne : (min_p > 0.f ? part_of(min_p, 1ull << kOne, exact) : 1ull);
     if (!exact) ++r.least;
     const float range = r.infinite ? 0.f : fminf(__fmul_rn(__fsub_rn(r.max, logit_of(static_cast<uint32_t>(last))), r.ch), kNone);
     r.bins = range > 1e-30f ? (kBins - 1) / range : 0.f;  // (else all in one)
@@ -1050,11 +1051,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_
     reduce_bins<NT>(pt, rank, blocks);
 
     // ---- questions, until the first block has found the token
-    Chooser<NT, IN> ch{pt, ct, blocks, counts, top_k, top_p, 0.f};
-    if (rank == 0) {
-        ch.u = d.u_dev[t];
-        ch.load_bins(ch.w, ch.n, ch.before_w, ch.before_n, ch.z, ch.all_n);
-    }
+    Chooser<NT, IN> ch{pt, ct, blocks, counts, top_k, top_p, u};
+    if (rank == 0) ch.load_bins(ch.w, ch.n, ch.before_w, ch.before_n, ch.z, ch.all_n);
 #pragma unroll 1
     for (;;) {
         if (rank == 0 && !ch.go_on()) {
