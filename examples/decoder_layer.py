@@ -48,15 +48,16 @@ class DecoderLayer:
         self.experts = MoePlan(weights, H, I, E, k, T_max=T_max, strict=True)
         self.cache_ws, self.experts_ws = self.cache.new_workspace(), self.experts.new_workspace()
 
-    def __call__(self, x, residual, q_off, kv_len, pages, max_q):
+    def __call__(self, x, residual, q_off, kv_len, pages, max_q, parents=None):
         """x: the layer before's output, float32 or bfloat16 [N, H]; residual:
-        bfloat16 [N, H], updated in place.  Returns this layer's output, float32."""
+        bfloat16 [N, H], updated in place; parents: int32 [N] where the new tokens are
+        trees.  Returns this layer's output, float32."""
         hq, hkv, d = self.heads
         h = add_rms_norm(x, self.norm1, residual=residual)
         q, k, v = self.qkv(h, dtype=torch.bfloat16).view(-1, hq + 2 * hkv, d).split((hq, hkv, hkv), dim=1)
         step = (q_off, kv_len, pages, self.cache_ws, max_q)
-        q = self.cache.append(k, v, *step, q=q)
-        o = self.cache.attend(q, *step)
+        q = self.cache.append(k, v, *step, q=q, parents=parents)
+        o = self.cache.attend(q, *step, parents=parents)
         h = add_rms_norm(self.out(o.view(-1, hq * d)), self.norm2, residual=residual)
         return self.experts.step_logits(h, self.router(h), self.experts_ws)
 
