@@ -87,11 +87,22 @@ def _bad(msg):
     return MoeError(MOE_ERR_INVALID_ARG, msg)
 
 
-# The checks below run on every call, so they compare in one go and look for the
-# reason only where that fails.
+# The checks below run on every call, and the host bounds the small ones: what is
+# right passes in one expression of few lookups, and the reason is looked for where
+# that fails.
+_Tensor, _INT32, _FLOAT32 = torch.Tensor, torch.int32, torch.float32
+
+
 def _rows(t, dtypes, tail, name, n=None):
-    """Row stride, in elements, of a CUDA tensor [n, *tail] whose rows are
-    contiguous (only dimension 0 may be strided)."""
+    """Row stride, in elements, of a CUDA tensor [n, *tail] (one or two dimensions of
+    tail) whose rows are contiguous (only dimension 0 may be strided)."""
+    if type(t) is _Tensor and t.is_cuda and t.dtype in dtypes:
+        shape, stride = t.shape, t.stride()
+        if len(tail) == 2:
+            if len(shape) == 3 and shape[1:] == tail and stride[2] == 1 and stride[1] == tail[1] and (n is None or shape[0] == n):
+                return stride[0] if shape[0] > 1 else tail[0] * tail[1]
+        elif len(shape) == 2 and shape[1] == tail[0] and stride[1] == 1 and (n is None or shape[0] == n):
+            return stride[0] if shape[0] > 1 else max(tail[0], 1)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise _bad(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -108,8 +119,7 @@ def _rows(t, dtypes, tail, name, n=None):
 
 
 def _need_out(t, dtype, shape, device, name):
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and
-            t.is_contiguous()):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         _need(t, dtype, name)
         raise _bad(f"{name} {tuple(t.shape)} on {t.device} is not {tuple(shape)} on {device}")
 
@@ -312,20 +322,23 @@ class KVCache:
 
     def _step(self, q_off, kv_len, pages, ws, N, max_q):
         """The batch description; checks the step's arrays and the workspace."""
-        B = kv_len.shape[0] if isinstance(kv_len, torch.Tensor) and kv_len.dim() == 1 else -1
+        dev = self.device
+        if isinstance(kv_len, _Tensor) and isinstance(q_off, _Tensor) and isinstance(pages, _Tensor):
+            one, two = kv_len.shape, pages.shape
+            if (len(one) == 1 and len(two) == 2 and one[0] == two[0] and q_off.shape == (one[0] + 1,) and
+                    kv_len.dtype is _INT32 and q_off.dtype is _INT32 and pages.dtype is _INT32 and
+                    kv_len.device == dev and q_off.device == dev and pages.device == dev and
+                    kv_len.is_contiguous() and q_off.is_contiguous() and pages.is_contiguous()):
+                self._need_ws(ws)
+                return C.byref(moe_kv_batch(q_off.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), two[1], one[0], N, max_q))
         for name, t in (("q_off", q_off), ("kv_len", kv_len), ("pages", pages)):
-            if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == self.device and
-                    t.is_contiguous()):
-                _need(t, torch.int32, name)
-                _same_device(self.device, **{name: t})
-        if B < 0 or q_off.shape != (B + 1,) or pages.dim() != 2 or pages.shape[0] != B:
-            raise _bad(f"shapes q_off {tuple(q_off.shape)}, kv_len {tuple(kv_len.shape)}, pages {tuple(pages.shape)} "
-                       "are not [B + 1], [B], [B, max_pages]")
-        self._need_ws(ws)
-        return C.byref(moe_kv_batch(q_off.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, N, max_q))
+            _need(t, torch.int32, name)
+            _same_device(dev, **{name: t})
+        raise _bad(f"shapes q_off {tuple(q_off.shape)}, kv_len {tuple(kv_len.shape)}, pages {tuple(pages.shape)} "
+                   "are not [B + 1], [B], [B, max_pages]")
 
     def _need_ws(self, ws):
-        if not (isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.device == self.device and
+        if not (isinstance(ws, _Tensor) and ws.dtype is torch.uint8 and ws.device == self.device and
                 ws.is_contiguous() and ws.numel() >= self._ws_bytes):
             _need(ws, torch.uint8, "ws")
             _same_device(self.device, ws=ws)
@@ -454,24 +467,12 @@ class KVCache:
         return pages_out, kv_len_out
 
     def _need_int32(self, t, shape, name):
-        if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == self.device and t.shape == shape and
-                t.is_contiguous()):
-            _need(t, torch.int32, name)
-            _same_device(self.device, **{name: t})
-            raise _bad(f"{name} {tuple(t.shape)} is not {shape}")
+        _need_out(t, _INT32, shape, self.device, name)
 
     def check(self, ws, stream=None) -> int:
         """Synchronise and return the device status (0 = MOE_OK); clears it."""
         self._need_ws(ws)
         return int(_library().moe_kv_check(self.handle, ws.data_ptr(), _handle(stream, self.device)))
-
-
-def _setting(v, dtype, T, device, name):
-    """(device pointer, value) of a setting of the sampling: a tensor [T], or a number for all rows."""
-    if isinstance(v, torch.Tensor):
-        _need_out(v, dtype, (T,), device, name)
-        return v.data_ptr(), 0
-    return None, v
 
 
 def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, prob=None, return_prob: bool = False,
@@ -485,21 +486,26 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise _bad("logits must be a CUDA tensor [T, V]")
     T, V = logits.shape
-    stride = _rows(logits, (torch.float32, torch.bfloat16), (V,), "logits")
-    dev = logits.device
+    stride = _rows(logits, (_FLOAT32, torch.bfloat16), (V,), "logits")
+    dev, one = logits.device, (T,)
     handle = _handle(stream, dev)
-    _need_out(u, torch.float32, (T,), dev, "u")
-    f32 = torch.float32
-    settings = (*_setting(temperature, f32, T, dev, "temperature"), *_setting(top_k, torch.int32, T, dev, "top_k"),
-                *_setting(top_p, f32, T, dev, "top_p"), *_setting(min_p, f32, T, dev, "min_p"))
+    _need_out(u, _FLOAT32, one, dev, "u")
+    settings = []
+    for v, dtype, name in ((temperature, _FLOAT32, "temperature"), (top_k, _INT32, "top_k"), (top_p, _FLOAT32, "top_p"),
+                           (min_p, _FLOAT32, "min_p")):
+        if isinstance(v, _Tensor):
+            _need_out(v, dtype, one, dev, name)
+            settings += (v.data_ptr(), 0)
+        else:
+            settings += (None, v)
     if out is None:
-        out = _empty((T,), torch.int32, dev, stream)
+        out = _empty(one, _INT32, dev, stream)
     else:
-        _need_out(out, torch.int32, (T,), dev, "out")
+        _need_out(out, _INT32, one, dev, "out")
     if prob is not None:
-        _need_out(prob, f32, (T,), dev, "prob")
+        _need_out(prob, _FLOAT32, one, dev, "prob")
     elif return_prob:
-        prob = _empty((T,), f32, dev, stream)
+        prob = _empty(one, _FLOAT32, dev, stream)
     d = moe_sample_desc(logits.data_ptr(), stride, logits.dtype == torch.bfloat16, T, V, u.data_ptr(), *settings,
                         out.data_ptr(), _ptr(prob))
     st = _library().moe_sample(C.byref(d), handle)
