@@ -228,6 +228,57 @@ __device__ __forceinline__ float *part_at(float *part, int TR, int row, int d)
     return part + 2 * TR + ((d >> 2) * TR + row) * 4 + (d & 3);
 }
 
+// The output of R rows of a tile (of TR, the others are none of the sequence's) from the partial
+// results of blocks c0 .. c1: a thread has one row and every (NT / R)-th group of four columns
+// of it; the loads of A blocks go out together.  (What a block writes comes back at 64 bytes a
+// cycle, the rate of an SM: 15 blocks' results of 64 rows of 128 take 8000 cycles with all
+// threads at work, 16000 with the half that 128 rows would leave.)
+template <int D, int NT, int TR, int R>
+__device__ __forceinline__ void join_rows(const AttendParams &p, const Segment &s, int c0, int c1, int rows, int q0, int G, float gain,
+                                          int tid)
+{
+    constexpr int IT = (R * (D / 4) + NT - 1) / NT, LOADS = TR == 128 ? 16 : 8, A = IT >= LOADS ? 1 : LOADS / IT;
+    const int row = tid % R, g0 = tid / R, r = s.tile * TR + row;
+    if (r >= rows || g0 >= D / 4) return;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = c0; k0 <= c1; k0 += A) {
+        float m[A], l[A];
+        float4 v[A][IT];
+#pragma unroll
+        for (int x = 0; x < A; ++x) {
+            float *q = part_slot(p, min(k0 + x, c1), min(k0 + x, c1) == c0);
+            m[x] = k0 + x <= c1 ? __ldcg(q + row) : -INFINITY;
+            l[x] = k0 + x <= c1 ? __ldcg(q + TR + row) : 0.f;
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+                v[x][i] = __ldcg(reinterpret_cast<const float4 *>(part_at(q, TR, row, 4 * (g0 + i * (NT / R)))));
+        }
+#pragma unroll
+        for (int x = 0; x < A; ++x) {
+            const float mn = fmaxf(M, m[x]), ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - ref), f1 = ex2(m[x] - ref);
+            L = L * f0 + l[x] * f1;
+            M = mn;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                acc[i].x = acc[i].x * f0 + v[x][i].x * f1;
+                acc[i].y = acc[i].y * f0 + v[x][i].y * f1;
+                acc[i].z = acc[i].z * f0 + v[x][i].z * f1;
+                acc[i].w = acc[i].w * f0 + v[x][i].w * f1;
+            }
+        }
+    }
+    const float inv = inv_sum(gain, L);
+    uint16_t *o = out_row(p, q0, s.h, G, r);
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+        *reinterpret_cast<uint2 *>(o + 4 * (g0 + i * (NT / R))) =
+            make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+}
+
 // A tile cut between blocks: the last of them to arrive joins the partials of
 // all and writes the output.  The block's NT consumers, this thread the tid-th of
 // them, their partials written.
@@ -248,47 +299,13 @@ __device__ __forceinline__ void join_tile(const AttendParams &p, const Segment &
     asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
     if (!*last) return;
     __threadfence();
-    // a thread has one row and every (NT / TR)-th group of four columns of it; the
-    // loads of A blocks go out together
-    constexpr int IT = (TR * (D / 4) + NT - 1) / NT, A = IT >= 8 ? 1 : 8 / IT;
-    const int row = tid % TR, g0 = tid / TR, r = s.tile * TR + row;
-    if (r >= rows || g0 >= D / 4) return;
-    float M = -INFINITY, L = 0.f;
-    float4 acc[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = c0; k0 <= c1; k0 += A) {
-        float m[A], l[A];
-        float4 v[A][IT];
-#pragma unroll
-        for (int x = 0; x < A; ++x) {
-            float *q = part_slot(p, min(k0 + x, c1), min(k0 + x, c1) == c0);
-            m[x] = k0 + x <= c1 ? __ldcg(q + row) : -INFINITY;
-            l[x] = k0 + x <= c1 ? __ldcg(q + TR + row) : 0.f;
-#pragma unroll
-            for (int i = 0; i < IT; ++i)
-                v[x][i] = __ldcg(reinterpret_cast<const float4 *>(part_at(q, TR, row, 4 * (g0 + i * (NT / TR)))));
-        }
-#pragma unroll
-        for (int x = 0; x < A; ++x) {
-            const float mn = fmaxf(M, m[x]), ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - ref), f1 = ex2(m[x] - ref);
-            L = L * f0 + l[x] * f1;
-            M = mn;
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                acc[i].x = acc[i].x * f0 + v[x][i].x * f1;
-                acc[i].y = acc[i].y * f0 + v[x][i].y * f1;
-                acc[i].z = acc[i].z * f0 + v[x][i].z * f1;
-                acc[i].w = acc[i].w * f0 + v[x][i].w * f1;
-            }
-        }
-    }
-    const float inv = inv_sum(gain, L);
-    uint16_t *o = out_row(p, q0, s.h, G, r);
-#pragma unroll
-    for (int i = 0; i < IT; ++i)
-        *reinterpret_cast<uint2 *>(o + 4 * (g0 + i * (NT / TR))) =
-            make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+    const int left = rows - s.tile * TR;
+    if (TR == 128 && left <= 32)
+        join_rows<D, NT, TR, (TR < 32 ? TR : 32)>(p, s, c0, c1, rows, q0, G, gain, tid);
+    else if (TR == 128 && left <= 64)
+        join_rows<D, NT, TR, (TR < 64 ? TR : 64)>(p, s, c0, c1, rows, q0, G, gain, tid);
+    else
+        join_rows<D, NT, TR, TR>(p, s, c0, c1, rows, q0, G, gain, tid);
 }
 
 // 2^e * f covers a page's v scale: the exponent that the running maximum adds to
