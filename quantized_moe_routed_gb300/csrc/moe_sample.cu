@@ -24,12 +24,14 @@
 // counted by their value first, of which there are few, where a block has many: each
 // value is weighed once.
 //
-// Few rows are bound by latency: one of 65543 fp32 logits takes 21 us with top-k and top-p, of which the
-// weights take 5, adding up the bins 3, the list 4, each further target 1.5 (a barrier of the
-// cluster takes 0.5, a pass over the 8 blocks' parts 3); 24 such rows 37 us.  Many rows are
-// bound by the integer units (80 operations a weight, 45 a small one), 16-bit ones by the
-// shared memory's atomics (8 cycles for a warp's): 256 rows of 131075 take 279 us in fp32, 90 us in bf16
-// (205 us with every token weighed), 1.7 turns of a row an SM.
+// Few rows are bound by latency: one of 65543 fp32 logits takes 21 us with top-k and top-p, of which
+// the weights take 5, adding up the bins 3, the list 4, each further target 1.5 (a barrier of the
+// cluster takes 0.5); 24 such rows of settings of their own 36 us.  Many rows are bound by the integer
+// units (80 operations a weight, 45 a small one), 16-bit ones by the shared memory's atomics (8
+// cycles for a warp's): 256 rows of 131075 take 283 us in fp32, 85 us in bf16 (205 us with
+// every token weighed), which are two turns of a row an SM: 152 rows take 48 us.  Code that is there
+// once matters: with the passes unrolled into each other, 2.5 MB of objects, one
+// row took 26 to 30 us, the instruction cache's misses.
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -981,17 +983,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_
         if (counts) atomicAdd(pt.cnt + bin, count);
     };
     if (counted && !r.infinite) {
+        // (neighbouring words to neighbouring threads: values that occur lie side by side)
 #pragma unroll 1
-        for (int i = tid; i < kCounters / 8; i += NT) {
-            const uint4 c = reinterpret_cast<const uint4 *>(counters)[i];
-            if ((c.x | c.y | c.z | c.w) == 0) continue;
+        for (int i = tid; i < kCounters / 2; i += NT) {
+            uint32_t c = counters[i];
 #pragma unroll 1
-            for (int y = 0; y < 8; ++y) {
-                const uint32_t m = (y & 4 ? (y & 2 ? c.w : c.z) : (y & 2 ? c.y : c.x)) >> (16 * (y & 1)) & 0xFFFFu;
-                if (m == 0) continue;
+            for (int y = 0; c != 0; ++y, c >>= 16) {
+                if ((c & 0xFFFFu) == 0) continue;
                 float x, e;
-                exponent(r, __uint_as_float(static_cast<uint32_t>(8 * i + y) << 16), x, e);
-                into_bin(x, e, m);
+                exponent(r, __uint_as_float(static_cast<uint32_t>(2 * i + y) << 16), x, e);
+                into_bin(x, e, c & 0xFFFFu);
             }
         }
     } else {
@@ -1106,9 +1107,10 @@ cudaError_t launch_sample(const moe_sample_desc &d, int num_sms, cudaStream_t st
         while (blocks < kMaxCluster && d.V > 4096 * blocks && 2LL * d.T * blocks <= room) blocks *= 2;
         return Params{d, (d.V + blocks - 1) / blocks, blocks};
     };
-    // Counters leave room for one block an SM, and pay where it has much to count.  Measured, with them
-    // and without: parts of 65543, 67 / 152 us (152 rows) and 54 / 85 (64 rows of two parts); of 32769,
-    // 39 / 52 (24 rows of four); of 20000, 45 / 45 (64 rows of two); of 16385, 50 / 46 (16 rows of eight).
+    // Counters leave room for one block an SM, and pay where it has much to count.  Measured with rows of
+    // settings of their own, with counters and without: parts of 131075, 67 / 152 us (152 rows); of 65538,
+    // 54 / 85 (64 rows of two parts); of 32769, 39 / 52 (24 rows of four); of 20000, 45 / 45 (64 rows of
+    // two); of 16385, 50 / 46 (16 rows of eight).
     const Params c = split(num_sms), p = split(2 * num_sms);
     if (!d.bf16) return launch_one<float, 512, false>(p, st);
     return c.part >= 24576 ? launch_one<uint16_t, 1024, true>(c, st) : launch_one<uint16_t, 512, false>(p, st);
