@@ -27,7 +27,7 @@
 // Few rows are bound by latency: one of 65543 fp32 logits takes 21 us with top-k and top-p, of which
 // the weights take 5, adding up the bins 3, the list 4, each further target 1.5 (a barrier of the
 // cluster takes 0.5); 24 such rows of settings of their own 36 us.  Many rows are bound by the integer
-// units (80 operations a weight, 45 a small one), 16-bit ones by the shared memory's atomics (8
+// units (80 operations a weight, 45 a small one), 16-bit ones by the shared memory's atomics (6
 // cycles for a warp's): 256 rows of 131075 take 283 us in fp32, 85 us in bf16 (205 us with
 // every token weighed), which are two turns of a row an SM: 152 rows take 48 us.  Code that is there
 // once matters: with the passes unrolled into each other, 2.5 MB of objects, one
@@ -565,7 +565,8 @@ __device__ __forceinline__ void answer(const Part<IN> &pt, const Row &r, Control
         });
     if (op == kRange) {
         gather_range<NT>(ct, a, b, rank, blocks);
-        __syncthreads();  // (all have read the question)
+        if (rank != 0) return;  // (the next question may be here already)
+        __syncthreads();        // (all have read this one)
         if (tid == 0) ct->klo = a, ct->khi = b;
         __syncthreads();
         return;
