@@ -45,6 +45,24 @@ __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, co
 // Tokens that row r of a sequence sees (r = new token * group + head).
 __device__ __forceinline__ int row_sees(int len, int n, int G, int r) { return max(len - n + r / G + 1, 0); }
 
+// The tokens of a page that a tree's token sees, a bit each: those before the tree, and of
+// the tree's, from slot -base of the page on, those in way (its own way to the root).
+__device__ __forceinline__ uint64_t tree_page(uint32_t way, int base)
+{
+    const uint64_t its = way;
+    if (base >= 0) return base < kPage ? its >> base : 0ull;
+    return base > -kPage ? its << -base | ((1ull << -base) - 1ull) : ~0ull;
+}
+
+// The token before new token i of a tree, -1: none; a parent that is not an earlier token counts as none.
+__device__ __forceinline__ int tree_parent(const AttendParams &p, int q0, int i)
+{
+    const int up = __ldg(p.parent + q0 + i);
+    if (up < i && up >= -1) return up;
+    atomicOr(p.c.ctrl + 2, kErrBadIndex);
+    return -1;
+}
+
 // The tokens of W pages from pg on that new token i of a tree sees, a bit each: those
 // before the tree (the sequence's first `past`), those on the way from i to the root.  A
 // parent is an earlier token, so the way back ends; one that is not counts as a

@@ -202,6 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
             // the tile's first row sees the least; of a tree's tokens each sees what is before the tree
             const int tile_sees = TREE ? max(len - n, 0) : row_sees(len, n, G, s.tile * TR);
 
+            // TREE: parents, a token a lane, loaded ahead of the pages that hold tokens of the tree
+            // (walking back from each row there, a load a token: 32 trees of 4 tokens after 8192 in 79.7 us
+            // against 76.4; without a tree 73).  A tree of more than 32 tokens comes here only
+            // under a max_q that is too small, and is walked.
+            int parent = -1;
+            if (TREE && lane < n) parent = tree_parent(p, q0, lane);
+
             float m[NX], l[NX];
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
@@ -256,30 +263,52 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
                 const bool edge = (pg + 1) * kPage > tile_sees;
                 const float lv = scale_log2(vs), pv = vs * 256.f;
                 float fs[NX], mx[NX];
-                uint64_t see[NX];  // TREE: the page's tokens that a row sees, the lane's first lowest
 #pragma unroll
                 for (int x = 0; x < NX; ++x) {
                     fs[x] = qs[x] * ks;
                     mx[x] = -INFINITY;
-                    see[x] = 0ull;
-                    if (TREE && edge) {
-                        uint64_t w[1] = {0ull};
-                        const int r = s.tile * TR + 8 * x + g;
-                        if (r < rows) tree_sees<1>(p, q0, len - n, r / G, pg, w);
-                        see[x] = w[0] >> (16 * t4 + 2 * NJ * half);
-                    }
                 }
-                if (TREE) __syncwarp();
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int x = 0; x < 2 * NX; ++x) {
                         sc[j][x] *= fs[x >> 1];
-                        if (edge && (TREE ? !((see[x >> 1] >> (2 * j + (x & 1))) & 1ull)
-                                          : pg * kPage + 16 * t4 + 2 * (NJ * half + j) + (x & 1) >= sees[x >> 1]))
-                            sc[j][x] = -INFINITY;
-                        mx[x >> 1] = fmaxf(mx[x >> 1], sc[j][x]);
+                        if (!TREE && edge && pg * kPage + 16 * t4 + 2 * (NJ * half + j) + (x & 1) >= sees[x >> 1]) sc[j][x] = -INFINITY;
+                        if (!TREE) mx[x >> 1] = fmaxf(mx[x >> 1], sc[j][x]);
                     }
+                if (TREE && edge) {
+                    // a token's way to the root: its parent's added, and on from the parent's parent
+                    uint32_t way = 1u << lane;
+                    if (n <= 32)
+                        for (int up = parent; __any_sync(0xffffffffu, up >= 0);) {
+                            const uint32_t its = __shfl_sync(0xffffffffu, way, up & 31);
+                            const int next = __shfl_sync(0xffffffffu, up, up & 31);
+                            if (up >= 0) way |= its, up = next;
+                        }
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) {  // the page's tokens that a row sees, the lane's first lowest
+                        const int r = s.tile * TR + 8 * x + g;
+                        uint64_t w[1];
+                        if (n <= 32) {
+                            const uint32_t its = __shfl_sync(0xffffffffu, way, (r / G) & 31);
+                            w[0] = tree_page(r < rows ? its : 0u, pg * kPage - (len - n));
+                        } else if (r < rows) {
+                            tree_sees<1>(p, q0, len - n, r / G, pg, w);
+                        }
+                        const uint32_t see = static_cast<uint32_t>(w[0] >> (16 * t4 + 2 * NJ * half));
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                if (!((see >> (2 * j + y)) & 1u)) sc[j][2 * x + y] = -INFINITY;
+                    }
+                    __syncwarp();
+                }
+                if (TREE)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int x = 0; x < 2 * NX; ++x) mx[x >> 1] = fmaxf(mx[x >> 1], sc[j][x]);
                 float ref[NX], alpha[NX];
                 bool grew = false;
 #pragma unroll
