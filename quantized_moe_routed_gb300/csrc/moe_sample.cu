@@ -28,7 +28,7 @@
 // the weights take 5, adding up the bins 3, the list 4, each further target 1.5 (a barrier of the
 // cluster takes 0.5); 24 such rows of settings of their own 36 us.  Many rows are bound by the integer
 // units (80 operations a weight, 45 a small one), 16-bit ones by the shared memory's atomics (6
-// cycles for a warp's): 256 rows of 131075 take 283 us in fp32, 85 us in bf16 (205 us with
+// cycles for a warp's): 256 rows of 131075 take 239 us in fp32, 85 us in bf16 (239 us with
 // every token weighed), which are two turns of a row an SM: 152 rows take 48 us.  Code that is there
 // once matters: with the passes unrolled into each other, 2.5 MB of objects, one
 // row took 26 to 30 us, the instruction cache's misses.
@@ -38,6 +38,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 namespace moe {
@@ -1102,19 +1104,39 @@ cudaError_t launch_one(const Params &p, cudaStream_t st)
 
 cudaError_t launch_sample(const moe_sample_desc &d, int num_sms, cudaStream_t st)
 {
-    // as many blocks a row as there is room for, each with 2048 logits or more
-    auto split = [&](int room) {
-        int blocks = 1;
-        while (blocks < kMaxCluster && d.V > 4096 * blocks && 2LL * d.T * blocks <= room) blocks *= 2;
-        return Params{d, (d.V + blocks - 1) / blocks, blocks};
+    // The split of a row with the least time by a model of it, in us: a block's fixed part, more in a cluster, and
+    // its logits, at 1.4 a thousand (counted 0.23); both grow with the blocks that share an SM or wait
+    // for one.  Fitted to 900 times of 16 to 1000 rows of 4000 to 262144 logits: a call takes 2 % more than with
+    // the best split of its own (18 % at worst).  Against as many blocks as the SMs hold, fp32: 256 rows of 131075
+    // 283 -> 239 us, 100 rows 148 -> 121, 76 rows of 32000 46 -> 35; bf16: 32 rows of 65543 40 -> 35, 100
+    // rows of 16000 37 -> 27.
+    struct Split {
+        int blocks;
+        double us;
     };
-    // Counters leave room for one block an SM, and pay where it has much to count.  Measured with rows of
-    // settings of their own, with counters and without: parts of 131075, 67 / 152 us (152 rows); of 65538,
-    // 54 / 85 (64 rows of two parts); of 32769, 39 / 52 (24 rows of four); of 20000, 45 / 45 (64 rows of
-    // two); of 16385, 50 / 46 (16 rows of eight).
-    const Params c = split(num_sms), p = split(2 * num_sms);
-    if (!d.bf16) return launch_one<float, 512, false>(p, st);
-    return c.part >= 24576 ? launch_one<uint16_t, 1024, true>(c, st) : launch_one<uint16_t, 512, false>(p, st);
+    auto best = [&](bool count) {
+        Split s{1, 0};
+        for (int b = 1; b <= kMaxCluster && (b == 1 || d.V > 2048 * b); b *= 2) {
+            const double logits = (d.V + b - 1) / b * 1e-3;
+            double more, us;  // blocks of an SM above the first
+            if (count) {  // each needs an SM's shared memory; clusters of 4 and 8 leave some SMs out
+                const int sms = b <= 2 ? num_sms : (b == 4 ? num_sms * 10 / 11 : num_sms * 10 / 13);
+                more = std::max(std::ceil(double(d.T) * b / sms) - 1, 0.);
+                us = (b > 1 ? 31 : 22) * (1 + 0.73 * more) + 0.23 * logits * (1 + 0.6 * more);
+            } else {
+                const double x = double(d.T) * b / num_sms;
+                more = std::max((x + std::ceil(x)) / 2 - 1, 0.);
+                us = (b > 1 ? 16 : 12) * (1 + 0.45 * more) + 1.4 * logits * (1 + 0.4 * more);
+            }
+            if (b == 1 || us < s.us) s = Split{b, us};
+        }
+        return s;
+    };
+    auto params = [&](const Split &s) { return Params{d, (d.V + s.blocks - 1) / s.blocks, s.blocks}; };
+    const Split p = best(false);
+    if (!d.bf16) return launch_one<float, 512, false>(params(p), st);
+    const Split c = best(true);
+    return c.us < p.us ? launch_one<uint16_t, 1024, true>(params(c), st) : launch_one<uint16_t, 512, false>(params(p), st);
 }
 
 }  // namespace moe
