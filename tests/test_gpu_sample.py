@@ -83,6 +83,29 @@ def test_flat_and_steep_rows(V, spread):
         _compare(y, _u(8, 6), k=V // 2, p=0.99)
 
 
+@pytest.mark.parametrize("T,V", [(3, 9001), (6, 131075), (24, 65543), (60, 131075), (20, 262144), (100, 20000), (170, 33000)])
+def test_the_same_however_rows_are_split(T, V):
+    """A row in a call of many, whose blocks have more of it and may count it by value, gets what it gets alone,
+    bit for bit; masked rows, rows of one value, of two, with infinities and of nothing among them."""
+    for half in (False, True):
+        x = _logits(T, V, T, half=half)
+        x[0] = 1.5
+        x[1, ::3] = -math.inf
+        x[2] = -2.0
+        x[2, V // 2:] = 1.0
+        if T > 5:
+            x[3] = -math.inf
+            x[4, V // 3], x[4, V - 1] = math.inf, math.inf
+            x[5, :V - 2] = math.nan
+        x = x.to(DEV)
+        u = torch.tensor(_u(T, V), device=DEV)
+        for t, k, p in ((1.0, 0, 1.0), (0.7, 0, 0.9), (1.2, 700, 0.95)):
+            tok, prob = sample(x, u, temperature=t, top_k=k, top_p=p, return_prob=True)
+            for i in list(range(min(T, 8))) + [T - 1]:
+                one, its = sample(x[i:i + 1], u[i:i + 1], temperature=t, top_k=k, top_p=p, return_prob=True)
+                assert int(one) == int(tok[i]) and float(its) == float(prob[i]), (i, half)
+
+
 def test_many_rows_of_16_bits():
     """Logits that are counted by value: whole rows of one value (more than a counter holds; twice 2^16), two
     values, infinite and masked and NaN ones beside ordinary rows."""
