@@ -11,10 +11,12 @@
 // unit that no two blocks share (no atomics, the same bits every run).  Another
 // block per (page, kv head) rotates the head group's queries.  The chain of
 // dependent loads (lengths, page id, old scale, codes) bounds it, for single tokens
-// (24 sequences: 5.0 us) and for chunks (4 x 4096 tokens of 32 + 16 heads of 128:
-// 37.9 us, 54% of the rate of a copy of the same bytes), where 64 registers a thread let
+// (24 sequences: 4.75 us) and for chunks (4 x 4096 tokens of 32 + 16 heads of 128:
+// 37.0 us, 55% of the rate of a copy of the same bytes), where 64 registers a thread let
 // two blocks of 512 share an SM; so the new tokens' loads do not wait for the
-// page's id, and v stays packed until it is coded (44.5 us otherwise).
+// page's id, v stays packed until it is coded (44.5 us otherwise), and what a thread reads
+// next, a head of the queries or the page's old codes of v, is under way before it is
+// needed (without: 5.0 and 37.9 us, 32 sequences of 60 tokens 17.1 instead of 15.4).
 #include "moe_internal.h"
 #include "moe_layer_internal.h"
 
@@ -53,9 +55,10 @@ struct Units {
     }
 };
 
-__device__ __forceinline__ void load8(float *v, const uint16_t *src)
+__device__ __forceinline__ uint4 at8(const uint16_t *src) { return *reinterpret_cast<const uint4 *>(src); }
+
+__device__ __forceinline__ void unpack8(float *v, const uint4 &a)
 {
-    const uint4 a = *reinterpret_cast<const uint4 *>(src);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         v[2 * j] = bf16_lo(u4w(a, j));
@@ -70,7 +73,7 @@ __device__ __forceinline__ void load_angles(const KvParams &c, float2 (&cs)[8], 
 {
     if (ROT == kNone || ROT == kOddHalves) return;
     const float2 *t = reinterpret_cast<const float2 *>(c.rope + static_cast<size_t>(pos) * c.rot_dim) + 8 * u;
-    if (ROT == kHalves) {  // eight pairs, or none (load_unit turns none)
+    if (ROT == kHalves) {  // eight pairs, or none (turn_unit turns none)
         if (8 * u >= c.rot_dim / 2) return;
 #pragma unroll
         for (int i = 0; i < 8; ++i) cs[i] = __ldg(t + i);
@@ -91,13 +94,13 @@ __device__ __forceinline__ float turn_b(float a, float b, float2 cs)
     return __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
 }
 
-// A head's unit, rotated.
+// A head's unit (lo, hi: its elements from c0 and from c1 on), rotated.
 template <Rot ROT>
-__device__ __forceinline__ void load_unit(const KvParams &c, float (&v)[16], const uint16_t *head, const Units<ROT> &un,
-                                          const float2 (&cs)[8], int pos)
+__device__ __forceinline__ void turn_unit(const KvParams &c, float (&v)[16], const uint4 &lo, const uint4 &hi,
+                                          const uint16_t *head, const Units<ROT> &un, const float2 (&cs)[8], int pos)
 {
-    load8(v, head + un.c0);
-    load8(v + 8, head + un.c1);
+    unpack8(v, lo);
+    unpack8(v + 8, hi);
     if (ROT == kNeighbours) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -251,10 +254,14 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
                 if (turns) load_angles<ROT>(c, cs, pos, u);
                 const uint16_t *src = p.q + (row0 + tok) * p.q_stride + h * G * D;
                 uint16_t *dst = p.q_out + (static_cast<size_t>(row0 + tok) * c.q_heads + h * G) * D;
+                // a head's loads are under way while the one before it is turned
+                uint4 lo = at8(src + un.c0), hi = at8(src + un.c1);
 #pragma unroll 1
                 for (int g = 0; g < G; ++g) {
                     float v[16];
-                    if (turns) load_unit<ROT>(c, v, src + g * D, un, cs, pos);
+                    const uint4 lo0 = lo, hi0 = hi;
+                    if (g + 1 < G) lo = at8(src + (g + 1) * D + un.c0), hi = at8(src + (g + 1) * D + un.c1);
+                    if (turns) turn_unit<ROT>(c, v, lo0, hi0, src + g * D, un, cs, pos);
                     // where partners are other elements of the token's UT lanes, all are read before
                     // any is written: the queries may be rotated in place
                     if (ROT == kOddHalves) __syncwarp(((1u << UT) - 1u) << (tid & 31 & ~(UT - 1)));
@@ -286,7 +293,8 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
             z[1] = zp[1];
             const int pos = angle_at(pos0 + tok);
             load_angles<ROT>(c, cs, pos, u);
-            load_unit<ROT>(c, x, p.k + (row0 + tok) * p.k_stride + h * D, un, cs, pos);
+            const uint16_t *kp = p.k + (row0 + tok) * p.k_stride + h * D;
+            turn_unit<ROT>(c, x, at8(kp + un.c0), at8(kp + un.c1), kp, un, cs, pos);
         }
         if (!turns || id < 0 || id >= c.n_pages) {
             if (tid == 0) atomicOr(c.ctrl + 2, kErrBadIndex);
@@ -294,6 +302,11 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
         }
         const size_t ph = static_cast<size_t>(id) * hk + h;
         const float old_ks = c.ks[ph], old_vs = c.vs[ph];
+        // v: a head dimension's codes are contiguous; sixteen tokens of one a thread, lo .. hi - 1 of them new
+        const int d = tid % D, s0 = (tid / D) * 16, lo = max(slot0 - s0, 0), hi = min(slot0 + cnt - s0, 16);
+        uint4 *vo = reinterpret_cast<uint4 *>(c.v + ph * (kPage * D) + d * kPage + s0);
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (lo < hi && (lo > 0 || hi < 16)) w = *vo;
         __syncthreads();  // the last page's readers of shared memory are done
         if (tid < kPage) bad_tok[tid] = 0;
         __syncthreads();
@@ -342,18 +355,9 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
             *dst = requant16(*dst, fk);
         }
         __syncthreads();
-        // v: a head dimension's codes are contiguous; sixteen tokens at a time
-        uint8_t *vo = c.v + ph * (kPage * D);
-        for (int i = tid; i < D * (kPage / 16); i += kThreads) {
-            const int d = i % D, s0 = (i / D) * 16;
-            const int lo = max(slot0 - s0, 0), hi = min(slot0 + cnt - s0, 16);  // the new ones
-            uint4 *dst = reinterpret_cast<uint4 *>(vo + d * kPage + s0);
-            if (lo >= hi && fv == 1.f) continue;
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (lo > 0 || hi < 16) {
-                w = *dst;
-                if (fv != 1.f) w = requant16(w, fv);
-            }
+        if (lo < hi || fv != 1.f) {
+            if (lo >= hi) w = *vo;
+            if (fv != 1.f) w = requant16(w, fv);
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kPage *D / 16, 2048 / (kPage * D / 16) / 2) mo
                 const uint32_t m = b <= a ? 0u : (0xFFFFFFFFu >> (32 - 8 * (b - a))) << (8 * a);
                 o[j] = (vt[(d * kStride + s0) / 4 + j] & m) | (u4w(w, j) & ~m);
             }
-            *dst = make_uint4(o[0], o[1], o[2], o[3]);
+            *vo = make_uint4(o[0], o[1], o[2], o[3]);
         }
         if (tid == 0) {
             c.ks[ph] = sk;
