@@ -84,8 +84,8 @@ constexpr Powers make_powers()
 __device__ const Powers kPowers = make_powers();
 
 // What the first block asks of all: the smallest and largest place in [klo, khi]; bins of
-// 2^shift places from klo on; a list of the tokens in [klo, khi].
-enum Op { kDone, kRange, kHist, kGather };
+// 2^shift places from klo on; a list of the tokens in [klo, khi]; the sum of the tail.
+enum Op { kDone, kRange, kHist, kGather, kTail };
 
 struct Control {
     u64 best[kMaxCluster], last[kMaxCluster];  // of each block: smallest and largest place (first: order) in range
@@ -93,6 +93,9 @@ struct Control {
     u64 klo, khi;                  // the question, and kRange's answer
     int op, shift;
     int n, all;                    // tokens in the list, tokens that were meant to be
+    uint32_t tail[2];              // of each block: what tokens of less than half a unit weigh, in units of 2^-63, low word first
+    uint32_t most_tail;            // units that they all together weigh at most; 0: there are none, or it is settled
+    float min_p;
     u64 powers[64];                // 2^(-j / 64) in units of 2^-61
     int powers32[64];              // and of 2^-30
     u64 scan_w[kMaxWarps], red[2 * kMaxWarps];
@@ -193,11 +196,10 @@ constexpr float kSmall = 16.f;   // from here on 32 bits are enough
 constexpr float kMagic = 12582912.f;        // 1.5 * 2^23: adding it leaves the nearest whole number in the low bits,
 constexpr int kMagicBits = 0x4B400000;      // above these
 
-// 2^-(p + e) in units of 2^-45, kSmall <= p < kNone (0 for another p).
-__device__ __forceinline__ uint32_t small_weight(const Control *ct, float p, float e)
+// 2^-(p + e) in units of 2^-ONE, ONE - 29 <= p < ONE + 1.5.
+template <int ONE>
+__device__ __forceinline__ uint32_t weight32(const Control *ct, float p, float e)
 {
-    const bool in = p >= kSmall && p < kNone;
-    if (!in) p = kSmall, e = 0.f;
     const float kf = __fmaf_rn(p, 64.f, kMagic);
     const int j = __float_as_int(kf) - kMagicBits;
     const float r = __fmaf_rn(__fsub_rn(kf, kMagic), -1.f / 64.f, p);
@@ -207,8 +209,17 @@ __device__ __forceinline__ uint32_t small_weight(const Control *ct, float p, flo
     const int dq = __float2int_rn(__fmul_rn(s, 4294967296.f));
     const int t = ct->powers32[j & 63];
     const uint32_t w = static_cast<uint32_t>(t + __mulhi(t, dq));
-    const int n = (j >> 6) - (kOne - 30);
-    return in ? ((w >> (n - 1)) + 1u) >> 1 : 0u;
+    const int n = (j >> 6) - (ONE - 30);
+    return ((w >> (n - 1)) + 1u) >> 1;
+}
+
+// 2^-(p + e) in units of 2^-45, kSmall <= p < kNone (0 for another p).
+__device__ __forceinline__ uint32_t small_weight(const Control *ct, float p, float e)
+{
+    const bool in = p >= kSmall && p < kNone;
+    if (!in) p = kSmall, e = 0.f;
+    const uint32_t w = weight32<kOne>(ct, p, e);
+    return in ? w : 0u;
 }
 
 // The same for any p.
@@ -431,6 +442,38 @@ __device__ __forceinline__ void add_weight(uint32_t *lo, uint32_t *hi, int bin, 
     if (b) atomicAdd(hi + bin, b);
 }
 
+// A token whose weight rounds to no unit is in no bin and is never given.  A long tail of such
+// tokens still adds up, 2^18 of them to 2^-28, and decides where equal logits meet a border exactly.  So
+// where a target lies nearer to the end of the token found than a tail can be, the tail is added up, in units
+// of 2^-63 (from 2^-63.5 down a weight is none), and the target is looked for again.  (Added up in every row
+// that can have one, in the first pass, it cost 2 to 4 % of all calls; so hardly any pays for it.)
+constexpr int kTailOne = 63;
+constexpr float kTailFrom = 45.5f, kTailEnd = 63.5f;
+template <int NT, typename IN>
+__device__ __noinline__ void add_tail(Control *ct, const IN *l, int n, float max, float ch, float cl)
+{
+    const Part<IN> pt{l, n, 0, nullptr, nullptr, nullptr, nullptr, nullptr};
+    Row r;
+    r.max = max, r.ch = ch, r.cl = cl;
+    bool exact = true;
+    const float min_p = ct->min_p;
+    uint32_t least = min_p > 0.f ? static_cast<uint32_t>(part_of(min_p, 1ull << kTailOne, exact)) : 1u;
+    if (!exact || least == 0) ++least;
+    each_four<NT>(pt, [&](const float(&v)[4]) {
+        uint32_t sum = 0;  // (at most 2^17 a token)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x, e;
+            exponent(r, v[i], x, e);
+            const bool in = x >= kTailFrom && x < kTailEnd && small_weight(ct, x, e) == 0;
+            const uint32_t w = weight32<kTailOne>(ct, in ? x : kTailFrom, in ? e : 0.f);
+            if (in && w >= least) sum += w;
+        }
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (sum != 0 && (threadIdx.x & 31) == 0) add_weight(ct->tail, ct->tail + 1, 0, sum);
+    });
+}
+
 template <int NT, typename IN>
 __device__ __forceinline__ void clear_bins(const Part<IN> &pt)
 {
@@ -508,6 +551,14 @@ __device__ __forceinline__ void answer(const Part<IN> &pt, const Row &r, Control
 {
     const int tid = threadIdx.x, op = ct->op, shift = ct->shift;
     const u64 klo = ct->klo, khi = ct->khi;
+    if (op == kTail) {
+        add_tail<NT>(ct, pt.l, pt.n, r.max, r.ch, r.cl);
+        if (blocks > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        return;
+    }
     if (op == kHist) clear_bins<NT>(pt);
     if (tid == 0) ct->n = 0;
     __syncthreads();
@@ -717,8 +768,11 @@ struct Chooser {
     __device__ __forceinline__ bool go_on()
     {
         for (;;) {
-            if (phase == 0) {  // a new target
-                if (!next_target()) return false;
+            if (phase == 0 || phase == 5) {  // a new target, the last one once more
+                if (phase == 5)
+                    target_with_tail();
+                else if (!next_target())
+                    return false;
                 find_bin(w, n, before_w, before_n, 0, 0);
                 klo = static_cast<u64>(ct->bin) << kBinShift, khi = klo + ((1ull << kBinShift) - 1);
                 bw = ct->base_w, bn = ct->base_n;
@@ -775,8 +829,39 @@ struct Chooser {
             } else {
                 look();
                 phase = rounds = 0;
+                const u64 upto = ct->base_w;  // the weights up to the token, its own included
+                const bool near = !count && t + ct->most_tail > upto && tail_counts();
+                __syncthreads();
+                if (near) {
+                    ask(kTail, 0);
+                    phase = 5;
+                    return true;
+                }
+                if (stage < 3) z = upto;
             }
         }
+    }
+
+    // Whether the target is a part of a sum that the tokens in no bin belong to and that can be told from others
+    // (top-k takes them all away, or leaves some, of which more is not known than their sum).
+    __device__ __forceinline__ bool tail_counts() const
+    {
+        if (ct->most_tail == 0 || (top_k > 0 && static_cast<uint32_t>(top_k) <= all_n)) return false;
+        return stage < 3 ? top_p > 0.f : !(top_p < 1.f) && u > 0.f && u < 1.f;
+    }
+
+    // The same target as a part of a sum that has the tail.  (Below the bins' own: top_p and u are 2^-24
+    // below 1, and the tail is 2^-28 of z at most.)
+    __device__ __forceinline__ void target_with_tail()
+    {
+        u64 f = 0;
+        for (int x = 0; x < blocks; ++x) f += static_cast<u64>(remote32(ct->tail + 1, x)) << 32 | remote32(ct->tail, x);
+        constexpr int kShift = kTailOne - kOne;
+        z += f >> kShift;
+        bool exact = true;
+        t = part_of(stage < 3 ? top_p : u, z, exact);
+        if (stage == 3 || !exact || (f & ((1ull << kShift) - 1)) != 0) ++t;
+        if (threadIdx.x == 0) ct->most_tail = 0;
     }
 
     // The target's place among the listed tokens in [klo, khi].
@@ -836,8 +921,6 @@ struct Chooser {
         }
         __syncthreads();
         key = ct->key_found, key_w = ct->w_found;
-        if (stage < 3) z = ct->base_w;  // (the weights up to it, its own included)
-        __syncthreads();
     }
 };
 
@@ -869,6 +952,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_
         ct->powers[tid] = v;
         ct->powers32[tid] = static_cast<int>((v + (1ull << 30)) >> 31);
     }
+    if (tid < 2) ct->tail[tid] = 0u;
     if (COUNT)
         for (int i = tid; i < kCounters / 8; i += NT) reinterpret_cast<uint4 *>(counters)[i] = make_uint4(0u, 0u, 0u, 0u);
     clear_bins<NT>(pt);
@@ -973,8 +1057,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const __grid_
     bool exact = true;
     r.least = min_p >= 1.f ? 1ull << kOne : (min_p > 0.f ? part_of(min_p, 1ull << kOne, exact) : 1ull);
     if (!exact) ++r.least;
-    const float range = r.infinite ? 0.f : fminf(__fmul_rn(__fsub_rn(r.max, logit_of(static_cast<uint32_t>(last))), r.ch), kNone);
+    const float reach = r.infinite ? 0.f : __fmul_rn(__fsub_rn(r.max, logit_of(static_cast<uint32_t>(last))), r.ch);
+    const float range = fminf(reach, kNone);
     r.bins = range > 1e-30f ? (kBins - 1) / range : 0.f;  // (else all in one)
+    if (tid == 0) {  // (min-p takes a tail away if it takes any token of a unit)
+        ct->most_tail = !(reach < kTailFrom) && r.least == 1 ? d.V / 2 + 2 : 0;
+        ct->min_p = min_p;
+    }
 
     // ---- the first pass: every token that counts into its bin
     const bool counts = top_k > 0 || top_p < 1.f;  // (else the one question needs none)
