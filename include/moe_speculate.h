@@ -100,10 +100,14 @@ moe_status_t moe_kv_fork(moe_kv_t kv, const int32_t *src_dev, const int32_t *fre
  * NaN counts as -infinity, and so as a token of weight 0, which is never given.  Where
  * the largest logit is +infinity the tokens at +infinity weigh 1, all others 0.  A row
  * of nothing but -infinity gives token -1 and prob 0.  u below 0 or NaN counts as 0, u of 1 and
- * above gives the last token that is left.
- * Weights are exact to 2^-36 of themselves and are summed in units of 2^-45 as whole
- * numbers, in any order the same: what is decided on a border (top-p's, the token's)
- * differs from the formula's only where the sums come within 2^-36 of it.
+ * above gives the last token that is left and weighs half of 2^-45 or more.
+ * Weights are whole numbers of units of 2^-45 (the largest weighs 1), which are summed the
+ * same in any order.  A weight is off by half a unit and 2^-36 of itself, one of less than
+ * 2^-16 by a unit at most; a sum over n tokens so by n units and 2^-36 of itself: 2^-27 at the
+ * worst, far less where errors of both signs meet.  What is decided on a border (min-p's, top-p's, the
+ * token's) differs from the formula's only where the sums come nearer to it than that.  A
+ * token of less than half a unit is never given, but counts in the sums that borders are
+ * parts of (from 2^-63.5 down it weighs nothing).
  * T >= 0 (0: a no-op), 1 <= V <= MOE_SAMPLE_MAX_VOCAB, stride >= V; pointers to their
  * elements' alignment. */
 #define MOE_SAMPLE_MAX_VOCAB 262144

@@ -14,9 +14,9 @@
 // them fit 64 bits): sums do not depend on the order of additions, so atomics give
 // the same bits every run, and borders are compared exactly.  A weight is
 // 2^-x, x = (max - l) log2(e) / t in two floats: 2^-(j / 64) from a table, the rest, below
-// 1/128, by its series; off by 2^-36 of itself, and from 2^-16 down, where most tokens are,
-// by half a unit (in 32 bits).  (fp32 would be off by 2^-24, and one row in a thousand
-// would get another token than the formula says.)
+// 1/128, by its series; off by half a unit and 2^-36 of itself, and from 2^-16 down, where
+// most tokens are and 32 bits hold it, by half a unit and 2^-29 of itself: a unit at most.  (fp32 would
+// be off by 2^-24, and one row in a thousand would get another token than the formula says.)
 //
 // A row belongs to a cluster of blocks, each with a part of it; the blocks add up their
 // bins through distributed shared memory and the first one decides: it puts questions
