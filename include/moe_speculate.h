@@ -69,14 +69,15 @@ moe_status_t moe_kv_compact(moe_kv_t kv, const int32_t *keep_dev, const int32_t 
  * and where fresh[c] >= 0 that page in the place of the one that the next token
  * goes to (page kv_len / MOE_KV_PAGE of the sequence), with a copy of its codes and scales
  * if it holds tokens; fresh[c] < 0 leaves the sequence's own page there, for one
- * child at most.  The full pages are shared.
+ * child at most (another that is left a partly filled one is flagged; a next page that holds no
+ * tokens yet is the caller's to give before they append).  The full pages are shared.
  *   src_dev, fresh_dev int32 [C]; kv_len_dev int32 [B]; pages_dev int32 [B, max_pages]
  *   kv_len_out_dev int32 [C], pages_out_dev int32 [C, max_pages], apart from the inputs
  * B and C 0 .. MOE_KV_MAX_SEQS (C = 0: a no-op).  A fresh page is in no sequence's table; it is not
  * used where the sequence fills its table.  A child whose src or length is out of
- * range, whose fresh page is not a page or an earlier child's too, or that needs a page whose id is
- * out of range, gets -1 in all of pages_out[c, :] and length 0, and is flagged for
- * moe_kv_check. */
+ * range, whose fresh page is not a page or an earlier child's too, that is left a partly filled page
+ * as an earlier child is, or whose page to copy is out of range, gets -1 in all of pages_out[c, :] and
+ * length 0, and is flagged for moe_kv_check. */
 moe_status_t moe_kv_fork(moe_kv_t kv, const int32_t *src_dev, const int32_t *fresh_dev, int C, const int32_t *kv_len_dev,
                          const int32_t *pages_dev, int max_pages, int B, int32_t *kv_len_out_dev, int32_t *pages_out_dev,
                          void *ws_dev, void *stream);

@@ -176,6 +176,10 @@ __global__ void __launch_bounds__(kMoveThreads) moe_kv_fork_kernel(const ForkPar
     const int ch = blockIdx.x, tid = threadIdx.x, h = blockIdx.y;
     const int s = p.src[ch], fresh = p.fresh[ch];
     int len = 0, tail = 0, page = -1;
+    // an earlier child that gets the same fresh page, or is left the same page (both would append to it if
+    // that is partly filled)
+    bool twin = false;
+    for (int i = tid; i < ch; i += kMoveThreads) twin |= fresh >= 0 ? p.fresh[i] == fresh : p.fresh[i] < 0 && p.src[i] == s;
     bool bad = s < 0 || s >= c.B || fresh >= c.n_pages;
     if (!bad) {
         len = c.kv_len[s];
@@ -188,8 +192,7 @@ __global__ void __launch_bounds__(kMoveThreads) moe_kv_fork_kernel(const ForkPar
             }
         }
     }
-    if (fresh >= 0)
-        for (int i = tid; i < ch; i += kMoveThreads) bad |= p.fresh[i] == fresh;
+    bad |= twin && (fresh >= 0 || len % kPage != 0);
     bad = __syncthreads_or(bad);
     if (!bad && page >= 0) {
         const size_t to = static_cast<size_t>(fresh) * c.kv_heads + h, from = static_cast<size_t>(page) * c.kv_heads + h;
