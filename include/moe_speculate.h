@@ -97,7 +97,7 @@ moe_status_t moe_kv_fork(moe_kv_t kv, const int32_t *src_dev, const int32_t *fre
  *   all rows.  temperature 1e-6 or less (or NaN): the token of rank 0; top_k <= 0: no
  *   limit; top_p >= 1 (or NaN): no limit, <= 0: rank 0 alone; min_p <= 0 (or NaN): no
  *   limit, >= 1: the tokens whose logit is the largest.
- *   token_dev  int32 [T]; prob_dev float [T] or NULL; apart from the inputs
+ *   token_dev  int32 [T]; prob_dev float [T] or NULL; apart from the inputs and each other
  * NaN counts as -infinity, and so as a token of weight 0, which is never given.  Where
  * the largest logit is +infinity the tokens at +infinity weigh 1, all others 0.  A row
  * of nothing but -infinity gives token -1 and prob 0.  u below 0 or NaN counts as 0, u of 1 and

@@ -3,6 +3,7 @@
 // moe_kv_attend.cu, moe_kv_attend_tc.cu, moe_kv_move.cu and moe_sample.cu.
 #include "moe_layer_host.h"
 
+#include <algorithm>
 #include <cmath>
 
 using moe::aligned;
@@ -28,11 +29,32 @@ moe_status_t check_tree(const moe_kv_batch *b, const int32_t *parent)
     return MOE_OK;
 }
 
-// Whether two arrays of int32 share memory.
-bool overlap(const int32_t *a, size_t na, const int32_t *b, size_t nb)
+// Whether two arrays of words share memory.
+bool overlap(const void *a, size_t na, const void *b, size_t nb)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + 4 * nb && y < x + 4 * na;
+}
+
+// Whether T words at `out` share memory with one of the T rows of logits (between rows they may lie).
+bool in_logits(const moe_sample_desc &d, const void *out)
+{
+    const uint64_t size = d.bf16 ? 2 : 4, T = static_cast<uint64_t>(d.T), row = size * d.V;
+    const uint64_t step = size * std::min(static_cast<uint64_t>(d.stride), uint64_t(1) << 56);  // (past any address)
+    const uint64_t a = reinterpret_cast<uintptr_t>(out), b = a + 4 * T, base = reinterpret_cast<uintptr_t>(d.logits_dev);
+    const uint64_t r = a < base + row ? 0 : (a - base - row) / step + 1;  // the first row that ends behind a
+    return r < T && base + r * step < b;
+}
+
+// Whether T words at `out` lie in one of the inputs.
+bool in_inputs(const moe_sample_desc &d, const void *out)
+{
+    const size_t T = static_cast<size_t>(d.T);
+    for (const void *in : {static_cast<const void *>(d.u_dev), static_cast<const void *>(d.temperature_dev),
+                           static_cast<const void *>(d.top_k_dev), static_cast<const void *>(d.top_p_dev),
+                           static_cast<const void *>(d.min_p_dev)})
+        if (in && overlap(out, T, in, T)) return true;
+    return in_logits(d, out);
 }
 
 template <typename F>
@@ -154,6 +176,10 @@ moe_status_t moe_sample(const moe_sample_desc *desc, void *stream)
                             static_cast<const void *>(d.min_p_dev), static_cast<const void *>(d.token_dev),
                             static_cast<const void *>(d.prob_dev)})
         if (!aligned(ptr, 4)) return fail(MOE_ERR_MISALIGNED, "settings, u, token and prob need 4-byte alignment");
+    if (in_inputs(d, d.token_dev) || (d.prob_dev && in_inputs(d, d.prob_dev)))
+        return fail(MOE_ERR_INVALID_ARG, "an output lies in one of the inputs");
+    const size_t T = static_cast<size_t>(d.T);
+    if (d.prob_dev && overlap(d.token_dev, T, d.prob_dev, T)) return fail(MOE_ERR_INVALID_ARG, "the outputs overlap");
     moe::Device dev;
     const moe_status_t st = moe::query_device(-1, &dev);
     if (st != MOE_OK) return st;
