@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv_attend_kernel(const __grid
 #pragma unroll
                     for (int x = 0; x < NX; ++x) {  // the page's tokens that a row sees, the lane's first lowest
                         const int r = s.tile * TR + 8 * x + g;
-                        uint64_t w[1];
+                        uint64_t w[1] = {0ull};  // (a row past the sequence's sees nothing)
                         if (n <= 32) {
                             const uint32_t its = __shfl_sync(0xffffffffu, way, (r / G) & 31);
                             w[0] = tree_page(r < rows ? its : 0u, pg * kPage - (len - n));
