@@ -59,8 +59,8 @@ moe_status_t moe_kv_attend_tree(moe_kv_t kv, const void *q_dev, int64_t q_stride
  * smaller are requantised (nearest, ties to even; exact for scales that are powers of
  * two as far as E4M3's exponent reaches), the page's other codes as well.  Slots behind the kept tokens
  * hold anything (no NaN code in v that was not there).  A sequence whose entries are
- * out of range or not ascending, whose length is out of range, or that needs a
- * page whose id is, is left as it is, kv_len_out[b] = kv_len[b], and flagged for moe_kv_check. */
+ * out of range or not ascending, whose length is out of range, or where the id of a page is that a
+ * kept token comes from or goes to, is left as it is, kv_len_out[b] = kv_len[b], and flagged for moe_kv_check. */
 moe_status_t moe_kv_compact(moe_kv_t kv, const int32_t *keep_dev, const int32_t *n_keep_dev, int max_keep,
                             int32_t *kv_len_out_dev, const moe_kv_batch *batch, void *ws_dev, void *stream);
 

@@ -54,10 +54,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) moe_kv_compact_kernel(const C
         id[tid] = !bad && p0 + tid < c.max_pages ? c.pages[static_cast<size_t>(b) * c.max_pages + p0 + tid] : -1;
     __syncthreads();
     if (!bad && m > 0) {
-        if (tid < m) bad = mine < 0 || mine >= n || (tid > 0 && keep[tid - 1] >= mine);
-        // pages that hold a token that stays (a last one out of range is bad in any case)
-        const int pages = (past + min(max(keep[m - 1], 0), n - 1)) / kPage - p0 + 1;
-        if (tid < pages) bad |= id[tid] < 0 || id[tid] >= c.n_pages;
+        auto is_page = [&](int pos) {
+            const int t = pos / kPage - p0;
+            return id[t] >= 0 && id[t] < c.n_pages;
+        };
+        // the pages that a token comes from and goes to have to be some; those between may be anything
+        if (tid < m) bad = mine < 0 || mine >= n || (tid > 0 && keep[tid - 1] >= mine) || !is_page(past + mine) || !is_page(past + tid);
     }
     bad = __syncthreads_or(bad);
     if (h == 0 && tid == 0) {
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) moe_kv_compact_kernel(const C
     int j0 = 0;  // the first token that moves (all after it do)
     while (j0 < m && keep[j0] == j0) ++j0;
     if (j0 == m) return;
-    if (const int pages = (past + keep[m - 1]) / kPage - p0 + 1; tid < pages) {
+    if (const int pages = (past + keep[m - 1]) / kPage - p0 + 1; tid < pages && id[tid] >= 0 && id[tid] < c.n_pages) {
         const size_t ph = static_cast<size_t>(id[tid]) * c.kv_heads + h;
         ks[tid] = c.ks[ph];
         vs[tid] = c.vs[ph];
