@@ -490,6 +490,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
     dev, one = logits.device, (T,)
     handle = _handle(stream, dev)
     _need_out(u, _FLOAT32, one, dev, "u")
+    if type(top_k) is int and not 0 < top_k <= V:
+        top_k = 0  # (no limit, also past 32 bits)
     settings = []
     for v, dtype, name in ((temperature, _FLOAT32, "temperature"), (top_k, _INT32, "top_k"), (top_p, _FLOAT32, "top_p"),
                            (min_p, _FLOAT32, "min_p")):
