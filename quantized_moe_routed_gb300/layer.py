@@ -410,15 +410,17 @@ class KVCache:
             _check(st)
         return out
 
-    def compact(self, keep, n_keep, q_off, kv_len, pages, ws, max_q: int, kv_len_out=None, stream=None):
+    def compact(self, keep, n_keep, q_off, kv_len, pages, ws, max_q: int = 0, kv_len_out=None, stream=None):
         """Keep the accepted ones of each sequence's newest tokens (moe_kv_compact),
         those that a step appended with the same q_off, kv_len and pages: of sequence
         b's n the ones keep[b, :n_keep[b]] (int32 [B, K], ascending; n_keep int32 [B]),
         which move up to follow the tokens before them.  Returns the new lengths, int32
-        [B]; kv_len is left as it is (and kv_len_out is another array)."""
+        [B]; kv_len is left as it is (and kv_len_out is another array).  max_q may be given, so
+        that a step's arguments go to append, attend and compact alike; nothing depends on it."""
         dev = self.device
         handle = _handle(stream, dev)
-        step = self._step(q_off, kv_len, pages, ws, (1 << 30) // self.q_heads, max_q)
+        # (offsets are only subtracted here, no row is read by them: the most rows that a step can have bound them)
+        step = self._step(q_off, kv_len, pages, ws, (1 << 30) // self.q_heads, 0)
         B = kv_len.shape[0]
         if not isinstance(keep, torch.Tensor) or keep.dim() != 2:
             raise _bad("keep must be a CUDA tensor [B, K]")

@@ -40,3 +40,17 @@ def test_compact_needs_only_the_pages_that_it_reads_and_writes(past, keep):
         out = cache.compact(kept, n_keep, q_off, kv_len, p, ws, max_q=n)
         assert cache.check(ws) == binding.MOE_ERR_BAD_INDEX and out.tolist() == [past + n]
         assert torch.equal(cache.k.cpu(), bufs[0]) and torch.equal(cache.v.cpu(), bufs[1])
+
+
+# ----------------------------------------------------------------------------- arguments
+def test_compact_asks_for_no_max_q():
+    """Nothing depends on it: left out, or any number."""
+    step = base.Step([12, 3], [100, 67], seed=5)
+    bufs = base._pool(step, 2, 128, seed=5)
+    keep, n_keep = moves._table([[0, 4, 11], [1]])
+    *want, lens = spec.compact(bufs, step.pages, step.q_off.tolist(), step.L, [[0, 4, 11], [1]], [3, 1])
+    for more in ({}, dict(max_q=12), dict(max_q=1), dict(max_q=10 ** 6)):
+        cache = base._cache(bufs, 2, 2, 128)
+        ws = cache.new_workspace()
+        assert cache.compact(keep, n_keep, *step.dev(), ws, **more).tolist() == lens and cache.check(ws) == 0
+        assert moves._same(moves._values(cache), want)
