@@ -4,12 +4,9 @@
 #include "moe_layer_host.h"
 
 #include <algorithm>
-#include <cmath>
 
 using moe::aligned;
-using moe::check_device;
 using moe::check_kv;
-using moe::check_rows;
 using moe::fail;
 using moe::kv_params;
 using moe::launched;
