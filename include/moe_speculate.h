@@ -99,7 +99,8 @@ moe_status_t moe_kv_fork(moe_kv_t kv, const int32_t *src_dev, const int32_t *fre
  *   limit, >= 1: the tokens whose logit is the largest.
  *   token_dev  int32 [T]; prob_dev float [T] or NULL; apart from the inputs and each other
  * NaN counts as -infinity, and so as a token of weight 0, which is never given.  Where
- * the largest logit is +infinity the tokens at +infinity weigh 1, all others 0.  A row
+ * the largest logit is +infinity the tokens at +infinity weigh 1, all others 0; a token whose
+ * distance to the largest overflows fp32 weighs 0 (at temperatures above 1e36 too).  A row
  * of nothing but -infinity gives token -1 and prob 0.  u below 0 or NaN counts as 0, u of 1 and
  * above gives the last token that is left and weighs half of 2^-45 or more.
  * Weights are whole numbers of units of 2^-45 (the largest weighs 1), which are summed the

@@ -442,7 +442,8 @@ class KVCache:
         sequence src[c] (int32 [C]) of kv_len [B] and pages [B, max_pages].  fresh[c]
         (int32 [C]) is a free page that becomes the child's own for the tokens to come,
         with a copy of what the sequence's last page holds; -1 leaves the child the
-        sequence's own page (for one child at most).  Full pages are shared.
+        sequence's own page (for one child at most: a second one that is left a partly
+        filled page is flagged, and gets no pages).  Full pages are shared.
         Returns (pages, kv_len) of the children, int32 [C, max_pages] and [C]."""
         dev = self.device
         handle = _handle(stream, dev)
